@@ -8,18 +8,32 @@ layer's other half, quantize_w4a4_act: bf16 activations -> the NVFP4 act /
 ascales operand plus lora_act_in = x @ lora_down^T, in one pass over x.
 
 Python binding over the C ABI of libgemm_w4a4.so (include/gemm_w4a4.h).
+Around them, for a transformer block on MXFP4 weights: quantize_mxfp4_act (the
+MXFP4 producer), gemm_mxfp4_few (the MXFP4 layer for few rows), rotary_axes
+(rotary positions over several axes) and cross_attention (attention to keys of
+another length).
+
 PyTorch supplies device memory and the stream; every step of the operator runs
 in the library's HIP kernels. If the library is missing the calls raise.
 """
 from __future__ import annotations
 
+import functools
+
 from . import _native
+from ._native import (ATTENTION_MAX_HEAD_DIM, FEW_MAX_M, ROTARY_MAX_AXES, ROTARY_MAX_HEAD_DIM, AttentionArgs, RotaryArgs,
+                      cross_attention_raw, cross_attention_workspace, gemm_mxfp4_few_raw, quantize_mxfp4_raw,
+                      quantize_mxfp4_workspace, rotary_axes_raw)
 from ._native import (EALIGN, EDEVICE, EINVAL, ENOMEM, ESCRATCH, ELAUNCH, EOVERLAP, FORMATS, MAX_R, OK, QUANTIZE_MAX_R,
                       quantize_noalloc_raw, quantize_plan, quantize_raw,
                       gemm_mxfp4_f16_raw, gemm_mxfp4_raw, gemm_w4a4_f16_raw, gemm_w4a4_raw,
                       library_path, plan, plan_variant, run_raw, strerror, variants)
 
-__all__ = ["gemm_w4a4", "gemm_mxfp4", "quantize_w4a4_act", "quantize_raw", "quantize_noalloc_raw", "quantize_plan", "QUANTIZE_MAX_R", "gemm_w4a4_raw", "gemm_w4a4_f16_raw", "gemm_mxfp4_raw",
+__all__ = ["quantize_mxfp4_act", "gemm_mxfp4_few", "rotary_axes", "cross_attention", "quantize_mxfp4_raw",
+           "quantize_mxfp4_workspace", "gemm_mxfp4_few_raw", "rotary_axes_raw", "cross_attention_raw",
+           "cross_attention_workspace", "RotaryArgs", "AttentionArgs", "FEW_MAX_M", "ROTARY_MAX_AXES",
+           "ROTARY_MAX_HEAD_DIM", "ATTENTION_MAX_HEAD_DIM",
+           "gemm_w4a4", "gemm_mxfp4", "quantize_w4a4_act", "quantize_raw", "quantize_noalloc_raw", "quantize_plan", "QUANTIZE_MAX_R", "gemm_w4a4_raw", "gemm_w4a4_f16_raw", "gemm_mxfp4_raw",
            "gemm_mxfp4_f16_raw", "run_raw", "plan", "plan_variant", "variants", "strerror", "library_path", "GemmError", "OK",
            "EINVAL", "EALIGN", "ELAUNCH", "EOVERLAP", "EDEVICE", "ENOMEM", "ESCRATCH", "MAX_R", "FORMATS"]
 
@@ -69,7 +83,16 @@ def gemm_mxfp4(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, lora
                    out, stream, dtype)
 
 
-_BLOCK = {"nvfp4": 16, "mxfp4": 32}
+_BLOCK = {"nvfp4": 16, "mxfp4": 32, "mxfp4_few": 32}
+
+
+def gemm_mxfp4_few(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, lora_up=None,
+                   out=None, stream=None, dtype=None):
+    """Enqueue the fused MXFP4 operator for few rows (M <= FEW_MAX_M): arguments
+    and result as gemm_mxfp4, in a kernel that streams the weights once.
+    """
+    return _launch("mxfp4_few", act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up,
+                   out, stream, dtype)
 
 
 def _launch(fmt, act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out, stream,
@@ -118,7 +141,9 @@ def _launch(fmt, act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     with torch.cuda.device(device):
         f16 = dtype == torch.float16
-        if fmt == "nvfp4":
+        if fmt == "mxfp4_few":
+            call = functools.partial(gemm_mxfp4_few_raw, f16)
+        elif fmt == "nvfp4":
             call = gemm_w4a4_f16_raw if f16 else gemm_w4a4_raw
         else:
             call = gemm_mxfp4_f16_raw if f16 else gemm_mxfp4_raw
@@ -166,3 +191,188 @@ def quantize_w4a4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=Non
     if rc != OK:
         raise GemmError(rc)
     return act, ascales, (lora_act_in if R else None)
+
+
+_HALF = None
+
+
+def _f16(t, name):
+    """Whether a 16-bit floating tensor on a GPU is binary16 (else bfloat16)."""
+    global _HALF
+    if _HALF is None:
+        import torch
+        _HALF = {torch.bfloat16: False, torch.float16: True}
+    f16 = _HALF.get(t.dtype)
+    if f16 is None:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError("tensors must live on a GPU device")
+    return f16
+
+
+def _enqueue(device, stream, call, *args):
+    """call(*args, stream handle) with `device` current; raises on a nonzero code."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == device.index:
+        rc = call(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = call(*args, handle)
+    if rc != OK:
+        raise GemmError(rc)
+
+
+def _workspace(nbytes, device, stream):
+    """nbytes of device memory for a call on `stream`, and their address (None, 0: none needed).
+    The allocator hands memory out again in the order of the stream it was asked for."""
+    import torch
+    if nbytes == 0:
+        return None, 0
+    if stream is None or stream == torch.cuda.current_stream(device):
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t, t.data_ptr()
+
+
+def quantize_mxfp4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=None, stream=None):
+    """Enqueue the MXFP4 producer on `stream`: x bfloat16 or float16 [M, K]
+    (K % 32 == 0) -> act uint8 [M, K/2], ascales uint8 [K/32, M] (the operand of
+    gemm_mxfp4 and gemm_mxfp4_few) and, when lora_down [R, K] of x's type is
+    given, lora_act_in [M, R] = x @ lora_down^T of that type. Without lora_down
+    it also lays out weights [N, K]. Outputs are allocated when None.
+    Returns (act, ascales, lora_act_in or None)."""
+    import torch
+    f16 = _f16(x, "x")
+    device = x.device
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    M, K = x.shape
+    _check(x, "x", x.dtype, (M, K), device)
+    R = 0
+    if lora_down is not None:
+        R = lora_down.shape[0]
+        _check(lora_down, "lora_down", x.dtype, (R, K), device)
+    if act is None:
+        act = torch.empty((M, K // 2), dtype=torch.uint8, device=device)
+    else:
+        _check(act, "act", torch.uint8, (M, K // 2), device)
+    if ascales is None:
+        ascales = torch.empty((K // 32, M), dtype=torch.uint8, device=device)
+    else:
+        _check(ascales, "ascales", torch.uint8, (K // 32, M), device)
+    if R > 0:
+        if lora_act_in is None:
+            lora_act_in = torch.empty((M, R), dtype=x.dtype, device=device)
+        else:
+            _check(lora_act_in, "lora_act_in", x.dtype, (M, R), device)
+    with torch.cuda.device(device):
+        nbytes = _native.load().quantize_mxfp4_workspace(M, K, R)
+    if nbytes < 0:
+        raise GemmError(nbytes)
+    keep, ws = _workspace(nbytes, device, stream)
+    _enqueue(device, stream, quantize_mxfp4_raw, f16, x.data_ptr(), lora_down.data_ptr() if R else 0,
+             act.data_ptr(), ascales.data_ptr(), lora_act_in.data_ptr() if R else 0, M, K, R, ws, nbytes)
+    return act, ascales, (lora_act_in if R else None)
+
+
+def rotary_axes(x, positions, inv_freq, sections, interleaved=True, inverse=False, out=None, stream=None):
+    """Enqueue rotary positions over several axes on `stream`.
+
+    x bfloat16 or float16 [batch, tokens, heads, head_dim], any strides with a
+    dense last dimension (the rotated heads of a joint projection, say);
+    positions int32 [batch, tokens, axes] or [tokens, axes] (shared by the
+    batch); sections: pairs per axis, dealt in order; inv_freq float32
+    [sum(sections)], the angle per unit of position of each pair. Pairs are
+    elements (2j, 2j+1) when interleaved, else (j, j + P), P = sum(sections);
+    elements from 2P on are copied. inverse turns the other way: the gradient
+    of x from the gradient of the result. out: allocated (dense) when None; x
+    itself for in place. Returns out.
+    """
+    import torch
+    f16 = _f16(x, "x")
+    device = x.device
+    if x.dim() != 4:
+        raise ValueError("x must be [batch, tokens, heads, head_dim]")
+    B, L, H, D = x.shape
+    axes = len(sections)
+    if not 1 <= axes <= ROTARY_MAX_AXES:
+        raise ValueError(f"1 to {ROTARY_MAX_AXES} axes, got {axes}")
+    if positions.dtype != torch.int32 or inv_freq.dtype != torch.float32:
+        raise TypeError("positions must be int32 and inv_freq float32")
+    if tuple(positions.shape) not in ((B, L, axes), (L, axes)):
+        raise ValueError(f"positions must be [{B}, {L}, {axes}] or [{L}, {axes}], got {tuple(positions.shape)}")
+    if tuple(inv_freq.shape) != (sum(sections),) or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous, one value per pair")
+    if positions.device != device or inv_freq.device != device:
+        raise ValueError(f"positions and inv_freq must be on {device}")
+    if axes > 1 and positions.stride(-1) != 1 or x.stride(3) != 1 and D > 1:
+        raise ValueError("the last dimension of x and of positions must be dense")
+    if out is None:
+        out = torch.empty((B, L, H, D), dtype=x.dtype, device=device)
+    else:
+        if out.dtype != x.dtype or out.shape != x.shape or out.device != device:
+            raise ValueError("out must have x's type, shape and device")
+        if out.stride(3) != 1 and D > 1:
+            raise ValueError("the last dimension of out must be dense")
+    ps = positions.stride()
+    args = RotaryArgs(x.data_ptr(), out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), B, L, H, D, axes,
+                      tuple(sections), x.stride()[:3], out.stride()[:3], ps[:2] if len(ps) == 3 else (0, ps[0]),
+                      bool(interleaved), bool(inverse), f16)
+    _enqueue(device, stream, rotary_axes_raw, args)
+    return out
+
+
+def cross_attention(q, k, v, kv_lens=None, scale=None, return_lse=False, out=None, stream=None):
+    """Enqueue attention of q to keys and values of another length on `stream`.
+
+    q bfloat16 or float16 [batch, q_len, q_heads, head_dim]; k, v [batch,
+    kv_len, kv_heads, head_dim] of q's type, q_heads a multiple of kv_heads
+    (neighbouring query heads share a key head); any strides that are
+    multiples of 8 with a dense last dimension; head_dim a multiple of 8 up to
+    ATTENTION_MAX_HEAD_DIM. kv_lens int32 [batch] on the device: keys in use of
+    each sequence (None: all); rows without keys give 0. scale: default
+    head_dim ** -0.5. Returns out [batch, q_len, q_heads, head_dim] (allocated
+    dense when None), and with return_lse also the float32 log-sum-exp
+    [batch, q_heads, q_len] (-inf for rows without keys).
+    """
+    import torch
+    f16 = _f16(q, "q")
+    device = q.device
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be 4-D")
+    B, LQ, HQ, D = q.shape
+    LK, HKV = k.shape[1], k.shape[2]
+    for t, name, shape in ((k, "k", (B, LK, HKV, D)), (v, "v", (B, LK, HKV, D))):
+        if t.dtype != q.dtype:
+            raise TypeError(f"{name} must be {q.dtype}, got {t.dtype}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if kv_lens is not None:
+        _check(kv_lens, "kv_lens", torch.int32, (B,), device)
+    if out is None:
+        out = torch.empty((B, LQ, HQ, D), dtype=q.dtype, device=device)
+    elif out.dtype != q.dtype or out.shape != q.shape or out.device != device:
+        raise ValueError("out must have q's type, shape and device")
+    for t in (q, k, v, out):
+        if t.stride(3) != 1 and D > 1:
+            raise ValueError("the last dimension of q, k, v and out must be dense")
+    lse = torch.empty((B, HQ, LQ), dtype=torch.float32, device=device) if return_lse else None
+    args = AttentionArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0,
+                         kv_lens.data_ptr() if kv_lens is not None else 0, B, LQ, LK, HQ, HKV, D, q.stride()[:3],
+                         k.stride()[:3], v.stride()[:3], out.stride()[:3], D ** -0.5 if scale is None else scale, f16)
+    nbytes = cross_attention_workspace(args)
+    if nbytes < 0:
+        raise GemmError(nbytes)
+    keep, ws = _workspace(nbytes, device, stream)
+    args.workspace, args.workspace_bytes = ws, nbytes
+    _enqueue(device, stream, cross_attention_raw, args)
+    return (out, lse) if return_lse else out

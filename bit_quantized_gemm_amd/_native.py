@@ -41,6 +41,25 @@ class QuantizePlan(ctypes.Structure):
         return {f: getattr(self, f) for f in _QPLAN_FIELDS + ("scratch_bytes",)}
 
 
+class RotaryArgs(ctypes.Structure):
+    """rotary_axes_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p)] + \
+               [(f, ctypes.c_int) for f in ("batch", "tokens", "heads", "head_dim", "axes")] + \
+               [("sections", ctypes.c_int * 4), ("x_stride", ctypes.c_int64 * 3),
+                ("out_stride", ctypes.c_int64 * 3), ("pos_stride", ctypes.c_int64 * 2),
+                ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int), ("f16", ctypes.c_int)]
+
+
+class AttentionArgs(ctypes.Structure):
+    """cross_attention_t."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k", "v", "out", "lse", "kv_lens")] + \
+               [(f, ctypes.c_int) for f in ("batch", "q_len", "kv_len", "q_heads", "kv_heads", "head_dim")] + \
+               [(f, ctypes.c_int64 * 3) for f in ("q_stride", "k_stride", "v_stride", "out_stride")] + \
+               [("scale", ctypes.c_float), ("f16", ctypes.c_int), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64)]
+
+
 class Plan(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int) for f in _PLAN_FIELDS]
 
@@ -97,6 +116,21 @@ def load() -> ctypes.CDLL:
         lib.gemm_w4a4_run.restype = i
         lib.gemm_w4a4_plan_variant.argtypes = [i, i, i, i, i, i, ctypes.POINTER(Plan)]
         lib.gemm_w4a4_plan_variant.restype = i
+        i64 = ctypes.c_int64
+        for name in ("quantize_mxfp4_act", "quantize_mxfp4_act_f16"):
+            getattr(lib, name).argtypes = [vp] * 5 + [i, i, i, vp, i64, vp]
+            getattr(lib, name).restype = i
+        lib.quantize_mxfp4_workspace.argtypes = [i, i, i]
+        lib.quantize_mxfp4_workspace.restype = i64
+        for name in ("gemm_mxfp4_few", "gemm_mxfp4_few_f16"):
+            getattr(lib, name).argtypes = [vp] * 9 + [i, i, i, i, vp]
+            getattr(lib, name).restype = i
+        lib.rotary_axes.argtypes = [ctypes.POINTER(RotaryArgs), vp]
+        lib.rotary_axes.restype = i
+        lib.cross_attention.argtypes = [ctypes.POINTER(AttentionArgs), vp]
+        lib.cross_attention.restype = i
+        lib.cross_attention_workspace.argtypes = [ctypes.POINTER(AttentionArgs)]
+        lib.cross_attention_workspace.restype = i64
         lib.gemm_w4a4_strerror.argtypes = [i]
         lib.gemm_w4a4_strerror.restype = ctypes.c_char_p
         _lib = lib
@@ -147,6 +181,49 @@ def quantize_noalloc_raw(x, lora_down, act, ascales, lora_act_in, M, K, R, strea
     """Direct call of quantize_w4a4_act_noalloc (no device allocation; its
     scratch is a fixed array per GPU) with integer addresses; returns its code."""
     return load().quantize_w4a4_act_noalloc(x, lora_down, act, ascales, lora_act_in, M, K, R, stream)
+
+
+FEW_MAX_M = 64
+ROTARY_MAX_AXES = 4
+ROTARY_MAX_HEAD_DIM = 256
+ATTENTION_MAX_HEAD_DIM = 128
+
+
+def quantize_mxfp4_raw(f16, x, lora_down, act, ascales, lora_act_in, M, K, R, workspace, workspace_bytes,
+                       stream) -> int:
+    """Direct call of quantize_mxfp4_act (f16: its _f16 twin) with integer addresses; returns its code."""
+    fn = load().quantize_mxfp4_act_f16 if f16 else load().quantize_mxfp4_act
+    return fn(x, lora_down, act, ascales, lora_act_in, M, K, R, workspace, workspace_bytes, stream)
+
+
+def quantize_mxfp4_workspace(M: int, K: int, R: int) -> int:
+    """Workspace bytes quantize_mxfp4_act needs for (M, K, R) (host only)."""
+    n = load().quantize_mxfp4_workspace(M, K, R)
+    if n < 0:
+        raise ValueError(f"quantize_mxfp4_workspace: {strerror(n)} ({n})")
+    return n
+
+
+def gemm_mxfp4_few_raw(f16, act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out,
+                       M, N, K, R, stream) -> int:
+    """Direct call of gemm_mxfp4_few (f16: its _f16 twin) with integer addresses; returns its code."""
+    fn = load().gemm_mxfp4_few_f16 if f16 else load().gemm_mxfp4_few
+    return fn(act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out, M, N, K, R, stream)
+
+
+def rotary_axes_raw(args: "RotaryArgs", stream) -> int:
+    """Direct call of rotary_axes; returns its code."""
+    return load().rotary_axes(ctypes.byref(args), stream)
+
+
+def cross_attention_raw(args: "AttentionArgs", stream) -> int:
+    """Direct call of cross_attention; returns its code."""
+    return load().cross_attention(ctypes.byref(args), stream)
+
+
+def cross_attention_workspace(args: "AttentionArgs") -> int:
+    """Workspace bytes of a cross_attention call, or a negative code (host only)."""
+    return load().cross_attention_workspace(ctypes.byref(args))
 
 
 def quantize_plan(M: int, K: int, R: int) -> dict:

@@ -1,0 +1,178 @@
+// mxfp4_few.hip — gemm_mxfp4's operation for few rows (gemm_mxfp4_few in
+// gemm_w4a4.h):
+//
+// y[m,n] = wcscale[n] * sum_k A[m,k] W[n,k] + bias[n] + sum_r la[m,r] lu[r,n]
+//
+// Bound by the weight bytes, N (K/2 + K/32): every weight is read once, from
+// HBM straight into the registers that the matrix instruction takes, since no
+// two waves share one. A workgroup owns 16 columns; its waves split K in steps
+// of 128 and add their sums through LDS. v_mfma_scale_f32_16x16x128_f8f6f4
+// with FP4 operands: lane (c, g) holds row c, k = 32 g .. 32 g + 31 as 16 bytes
+// and that block's scale byte. The weights are its A operand (rows n) and the
+// activations, which stay in cache, its B operand (columns m), so that a lane
+// ends with 4 neighbouring columns n of one row m. Each wave adds its share
+// of the LoRA ranks to its own sums, after the factor wcscale that the LoRA
+// term does not take.
+#include <hip/hip_runtime.h>
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "gemm_w4a4.h"
+#include "w4a4_common.hpp"
+#include "w4a4_half.hpp"
+#include "w4a4_host.hpp"
+
+namespace w4a4 {
+
+__device__ __forceinline__ f32x4 mfma_fp4_16(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
+  typedef int v8i __attribute__((ext_vector_type(8)));
+  const v8i av = {int(a.x), int(a.y), int(a.z), int(a.w), 0, 0, 0, 0};   // FP4 uses the low 4 dwords
+  const v8i bv = {int(b.x), int(b.y), int(b.z), int(b.w), 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, int(sa), 0, int(sb));
+}
+
+constexpr int kFewWaves = 8;
+constexpr int kFewCols = 16;
+
+// MT: tiles of 16 rows (M <= 16 MT).
+template <bool F16, int MT>
+__global__ __launch_bounds__(kFewWaves * kWave) void mx_few_kernel(const Params p) {
+  constexpr int W = kFewWaves;
+  __shared__ f32x4 red[W * MT * kWave];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int M = p.M, N = p.N, K = p.K, R = p.R;
+  const int n0 = blockIdx.x * kFewCols;
+  const int kb_all = K >> 5;
+  const uint32_t rowbytes = uint32_t(K) >> 1;
+  // rows and columns past the edge repeat the last and are not stored
+  const int n = min(n0 + c, N - 1);
+  const uint8_t* w = p.wgt + uint32_t(n) * rowbytes + 16 * g;
+  const uint8_t* ws = p.wscales + n;
+  const uint8_t* a[MT];
+  const uint8_t* as[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = min(16 * t + c, M - 1);
+    a[t] = p.act + uint32_t(m) * rowbytes + 16 * g;
+    as[t] = p.ascales + m;
+  }
+  f32x4 acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int steps = (K + 127) >> 7;
+  for (int s = wave; s < steps; s += W) {
+    const int kb = 4 * s + g;
+    const bool live = kb < kb_all;      // K % 128 != 0: blocks past K are zeros of scale one
+    const u32x4 wv = live ? *reinterpret_cast<const u32x4*>(w + 64 * s) : u32x4{0u, 0u, 0u, 0u};
+    const uint32_t wsc = live ? ws[uint32_t(kb) * uint32_t(N)] : 127u;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const u32x4 av = live ? *reinterpret_cast<const u32x4*>(a[t] + 64 * s) : u32x4{0u, 0u, 0u, 0u};
+      const uint32_t asc = live ? as[t][uint32_t(kb) * uint32_t(M)] : 127u;
+      acc[t] = mfma_fp4_16(wv, av, acc[t], wsc, asc);
+    }
+  }
+  // lane (c, g): columns n0 + 4g + e of row 16 t + c
+  float wc[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) wc[e] = p.wcscale[min(n0 + 4 * g + e, N - 1)];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[t][e] *= wc[e];
+
+  // ranks r0 .. r0+31: lane (c, g) supplies ranks r0 + 8g .. +7 of column n
+  // (A) and of row m (B)
+  for (int r0 = 32 * wave; r0 < R; r0 += 32 * W) {
+    const int rr = r0 + 8 * g;
+    uint16_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = rr + i < R ? p.lora_up[uint32_t(rr + i) * uint32_t(N) + uint32_t(n)] : 0;
+    const u32x4 uv = {bf16_pair(u[0], u[1]), bf16_pair(u[2], u[3]), bf16_pair(u[4], u[5]), bf16_pair(u[6], u[7])};
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const uint16_t* la = p.lora_act_in + uint32_t(min(16 * t + c, M - 1)) * uint32_t(R);
+      uint16_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = rr + i < R ? la[rr + i] : 0;
+      const u32x4 vv = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+      acc[t] = mfma16<F16>(uv, vv, acc[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) red[(wave * MT + t) * kWave + lane] = acc[t];
+  __syncthreads();
+  for (int t = wave; t < MT; t += W) {
+    f32x4 y = red[t * kWave + lane];
+#pragma unroll
+    for (int q = 1; q < W; ++q) y += red[(q * MT + t) * kWave + lane];
+    const int m = 16 * t + c;
+    if (m >= M) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int col = n0 + 4 * g + e;
+      if (col < N) p.out[uint32_t(m) * uint32_t(N) + uint32_t(col)] = narrow<F16>(y[e] + p.bias[col]);
+    }
+  }
+}
+
+static bool few_sizes_ok(int M, int N, int K, int R) {
+  if (!(M >= 1 && M <= GEMM_MXFP4_FEW_MAX_M && N >= 1 && K >= 32 && K % 32 == 0 && R >= 0 && R <= GEMM_W4A4_MAX_R))
+    return false;
+  const int64_t lim = int64_t(1) << 31;
+  const int64_t m = M, n = N, k = K, r = R;
+  return m * k / 2 < lim && n * k / 2 < lim && m * n * 2 < lim && m * r * 2 < lim && r * n * 2 < lim;
+}
+
+template <bool F16>
+static int mx_few_run(const uint8_t* act, const uint8_t* ascales, const uint8_t* wgt, const uint8_t* wscales,
+                      const float* wcscale, const float* bias, const uint16_t* lora_act_in, const uint16_t* lora_up,
+                      uint16_t* out, int M, int N, int K, int R, void* stream) {
+  if (!few_sizes_ok(M, N, K, R)) return GEMM_W4A4_EINVAL;
+  const int rc = check_call(CallArgs{act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out, M, N, K, R, stream}, 32);
+  if (rc != GEMM_W4A4_OK) return rc;
+  const int dev_rc = check_device();
+  if (dev_rc != GEMM_W4A4_OK) return dev_rc;
+  Params p{};
+  p.act = act;
+  p.ascales = ascales;
+  p.wgt = wgt;
+  p.wscales = wscales;
+  p.wcscale = wcscale;
+  p.bias = bias;
+  p.lora_act_in = lora_act_in;
+  p.lora_up = lora_up;
+  p.out = out;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.R = R;
+  void* args[] = {&p};
+  const void* k = M <= 16 ? reinterpret_cast<const void*>(mx_few_kernel<F16, 1>)
+                : M <= 32 ? reinterpret_cast<const void*>(mx_few_kernel<F16, 2>)
+                          : reinterpret_cast<const void*>(mx_few_kernel<F16, 4>);
+  const hipError_t e = hipLaunchKernel(k, dim3((N + kFewCols - 1) / kFewCols), dim3(kFewWaves * kWave), args, 0,
+                                       static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? GEMM_W4A4_OK : GEMM_W4A4_ELAUNCH;
+}
+
+}  // namespace w4a4
+
+extern "C" int gemm_mxfp4_few(const uint8_t* act, const uint8_t* ascales, const uint8_t* wgt, const uint8_t* wscales,
+                              const float* wcscale, const float* bias, const uint16_t* lora_act_in,
+                              const uint16_t* lora_up, uint16_t* out, int M, int N, int K, int R, void* stream) {
+  return w4a4::mx_few_run<false>(act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out, M, N, K, R, stream);
+}
+
+extern "C" int gemm_mxfp4_few_f16(const uint8_t* act, const uint8_t* ascales, const uint8_t* wgt,
+                                  const uint8_t* wscales, const float* wcscale, const float* bias,
+                                  const uint16_t* lora_act_in, const uint16_t* lora_up, uint16_t* out, int M, int N,
+                                  int K, int R, void* stream) {
+  return w4a4::mx_few_run<true>(act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out, M, N, K, R, stream);
+}

@@ -329,6 +329,163 @@ int quantize_w4a4_act_noalloc(const uint16_t* x, const uint16_t* lora_down, uint
                               uint8_t* ascales, uint16_t* lora_act_in, int M, int K, int R,
                               void* stream);
 
+/*
+ * quantize_mxfp4_act / quantize_mxfp4_act_f16 — the producer of gemm_mxfp4's
+ * operand: 16-bit activations x to E2M1 codes and UE8M0 block scales, and the
+ * rank-R LoRA input, in one pass over x. With R = 0 it also lays out weights
+ * (rows n of wgt [N, K] in place of rows m).
+ *
+ *   x            uint16  [M, K]     bfloat16 (_f16: binary16) bit patterns (read)
+ *   lora_down    uint16  [R, K]     same type, one rank per row (read); may be NULL iff R == 0
+ *   act          uint8   [M, K/2]   written: two E2M1 codes per byte, low nibble = even k
+ *   ascales      uint8   [K/32, M]  written: UE8M0 scale of (m, k) at [k/32][m]
+ *   lora_act_in  uint16  [M, R]     written, x's type: sum_k x[m,k] * lora_down[r,k]
+ *                                   (float32 accumulation, rounded to nearest even);
+ *                                   may be NULL iff R == 0
+ *
+ * Per row and block of 32 consecutive k, the microscaling formats' rule: the
+ * scale is 2^(floor(log2 max|x|) - 2), so that the largest magnitude lands in
+ * [4, 8) and saturates at 6, the largest E2M1 value; the scale byte is that
+ * exponent + 127, at least 0; a code is the sign of x and the E2M1 magnitude
+ * nearest |x| / scale, ties to the even code (exact: the division is by a
+ * power of two). A block with a NaN or an infinity gets byte 0xFF and zero
+ * codes; a block of zeros byte 0.
+ *
+ * M >= 1; K >= 32 with K % 32 == 0; 0 <= R <= QUANTIZE_W4A4_MAX_R; every
+ * tensor below 2^31 bytes. Alignment: x, lora_down, act 16 bytes, lora_act_in
+ * 2, workspace 16. No output may overlap an input or another output.
+ *
+ * workspace: quantize_mxfp4_workspace(M, K, R) bytes of device memory that
+ * nothing else uses until the call's work on `stream` has finished (0: NULL is
+ * fine). Fewer: GEMM_W4A4_ESCRATCH. The call allocates and synchronises
+ * nothing. Results do not depend on what the workspace holds.
+ */
+int quantize_mxfp4_act(const uint16_t* x, const uint16_t* lora_down, uint8_t* act, uint8_t* ascales,
+                       uint16_t* lora_act_in, int M, int K, int R, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+int quantize_mxfp4_act_f16(const uint16_t* x, const uint16_t* lora_down, uint8_t* act, uint8_t* ascales,
+                           uint16_t* lora_act_in, int M, int K, int R, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+/* Workspace bytes for (M, K, R) on the current device, or GEMM_W4A4_EINVAL (host only). */
+int64_t quantize_mxfp4_workspace(int M, int K, int R);
+
+/*
+ * gemm_mxfp4_few / gemm_mxfp4_few_f16 — gemm_mxfp4's operation for few rows
+ * (1 <= M <= GEMM_MXFP4_FEW_MAX_M): the weights are streamed once past all
+ * rows instead of being tiled for many. Arguments, layouts, sizes, alignments
+ * and return codes are gemm_mxfp4's / gemm_mxfp4_f16's; the results agree
+ * with theirs up to the order of the float32 sums, not byte for byte. No
+ * workspace; deterministic.
+ */
+#define GEMM_MXFP4_FEW_MAX_M 64
+int gemm_mxfp4_few(const uint8_t* act, const uint8_t* ascales,
+                   const uint8_t* wgt, const uint8_t* wscales,
+                   const float* wcscale, const float* bias,
+                   const uint16_t* lora_act_in, const uint16_t* lora_up,
+                   uint16_t* out, int M, int N, int K, int R, void* stream);
+int gemm_mxfp4_few_f16(const uint8_t* act, const uint8_t* ascales,
+                       const uint8_t* wgt, const uint8_t* wscales,
+                       const float* wcscale, const float* bias,
+                       const uint16_t* lora_act_in, const uint16_t* lora_up,
+                       uint16_t* out, int M, int N, int K, int R, void* stream);
+
+/*
+ * rotary_axes — rotary positions over several axes (time, height, width, ...)
+ * applied to heads x [batch, tokens, heads, head_dim]. The P pairs of a head
+ * (P = the sum of sections, 2P <= head_dim) are dealt to the axes in order,
+ * sections[a] pairs to axis a. Pair j on axis a turns by
+ *
+ *     t = positions[batch, token, a] * inv_freq[j]        (radians)
+ *     (u, w) -> (u cos t - w sin t, u sin t + w cos t)
+ *
+ * where (u, w) are elements (2j, 2j+1) when interleaved, else (j, j + P).
+ * Elements from 2P on are copied. `inverse` turns by -t: the backward pass,
+ * since a rotation's transpose is the opposite rotation. The angle is reduced
+ * to one turn with the product's float32 rounding error carried along, so it
+ * holds for large positions; rotation in float32, rounded once.
+ *
+ * Strides are in elements; the last dimension is dense; positions' axes are
+ * dense (stride 1), with a stride per batch (0: shared) and per token. out may
+ * be x itself with the same strides (in place); any other overlap, or
+ * overlap with positions or inv_freq, is GEMM_W4A4_EOVERLAP. Strides are
+ * non-negative and out's may not make two elements share memory
+ * (GEMM_W4A4_EINVAL). x and out 2-byte, positions and inv_freq 4-byte aligned;
+ * interleaved needs an even head_dim (GEMM_W4A4_EINVAL) and pairs that start on
+ * 4 bytes (GEMM_W4A4_EALIGN).
+ * batch, tokens and heads may be 0: nothing is enqueued.
+ */
+#define ROTARY_AXES_MAX 4
+#define ROTARY_MAX_HEAD_DIM 256
+typedef struct {
+  const void* x;             /* 16-bit type, see f16 */
+  void* out;
+  const int32_t* positions;
+  const float* inv_freq;     /* [P] */
+  int batch, tokens, heads, head_dim;
+  int axes;                  /* 1 .. ROTARY_AXES_MAX */
+  int sections[ROTARY_AXES_MAX];   /* pairs per axis, each >= 0 */
+  int64_t x_stride[3];       /* batch, token, head */
+  int64_t out_stride[3];
+  int64_t pos_stride[2];     /* batch, token */
+  int interleaved, inverse;
+  int f16;                   /* 0: bfloat16, 1: binary16 */
+} rotary_axes_t;
+int rotary_axes(const rotary_axes_t* args, void* stream);
+
+/*
+ * cross_attention — attention of q [batch, q_len, q_heads, head_dim] to keys
+ * and values [batch, kv_len, kv_heads, head_dim] of another length:
+ *
+ *     out[b, i, h] = sum_j softmax_j(scale * q[b,i,h] . k[b,j,g]) v[b,j,g],
+ *     g = h / (q_heads / kv_heads),  j < kv_lens[b]
+ *
+ *   kv_lens   int32 [batch] on the device, or NULL: kv_len keys everywhere.
+ *             Values outside 0 .. kv_len are taken as the nearest of the two.
+ *             Keys and values from kv_lens[b] on are never read.
+ *   lse       float [batch, q_heads, q_len], written when not NULL: the natural
+ *             log of the sum of exp(scale * q . k) (joins attentions over
+ *             parts of the keys)
+ * A row without keys gives out 0 and lse -inf. Scores, softmax statistics and
+ * sums are float32; the weights exp(...) are rounded to the 16-bit type for
+ * the product with v.
+ *
+ * scale: positive, at most 1e30. head_dim: a multiple of 8, 8 .. CROSS_ATTENTION_MAX_HEAD_DIM; q_heads a
+ * multiple of kv_heads. Strides in elements, multiples of 8 (a dimension of
+ * size 1 excepted), non-negative, k's and v's token strides below 2^23; the
+ * last dimension is dense; all four tensors 16-byte aligned. q, k and v may
+ * repeat memory (stride 0); out may not (GEMM_W4A4_EINVAL) and out and lse may
+ * overlap nothing else (GEMM_W4A4_EOVERLAP). batch, q_len or q_heads 0:
+ * nothing is enqueued; kv_len 0: k and v may be NULL.
+ *
+ * workspace: cross_attention_workspace bytes of device memory, 16-byte
+ * aligned, that nothing else uses until the call's work on `stream` has
+ * finished (0: NULL is fine). Fewer: GEMM_W4A4_ESCRATCH. Few rows split the
+ * keys over workgroups and join the parts from there in a second launch, in a
+ * fixed order. Deterministic; no allocation, no synchronisation.
+ */
+#define CROSS_ATTENTION_MAX_HEAD_DIM 128
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  const int32_t* kv_lens;
+  int batch, q_len, kv_len, q_heads, kv_heads, head_dim;
+  int64_t q_stride[3];       /* batch, token, head */
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t out_stride[3];
+  float scale;
+  int f16;                   /* 0: bfloat16, 1: binary16 */
+  void* workspace;
+  int64_t workspace_bytes;
+} cross_attention_t;
+int cross_attention(const cross_attention_t* args, void* stream);
+/* Workspace bytes of this call on the current device (sizes only; no pointer is
+ * read), or GEMM_W4A4_EINVAL (host only). */
+int64_t cross_attention_workspace(const cross_attention_t* args);
+
 /* Static string for a return code (never NULL). */
 const char* gemm_w4a4_strerror(int code);
 
