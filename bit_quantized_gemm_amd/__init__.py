@@ -18,10 +18,9 @@ in the library's HIP kernels. If the library is missing the calls raise.
 """
 from __future__ import annotations
 
-import functools
-
 from . import _native
-from ._native import (ATTENTION_MAX_HEAD_DIM, FEW_MAX_M, ROTARY_MAX_AXES, ROTARY_MAX_HEAD_DIM, AttentionArgs, RotaryArgs,
+from ._native import (ATTENTION_MAX_HEAD_DIM, ATTENTION_PACK, FEW_MAX_M, ROTARY_MAX_AXES, ROTARY_MAX_HEAD_DIM,
+                      ROTARY_PACK, AttentionArgs, RotaryArgs,
                       cross_attention_raw, cross_attention_workspace, gemm_mxfp4_few_raw, quantize_mxfp4_raw,
                       quantize_mxfp4_workspace, rotary_axes_raw)
 from ._native import (EALIGN, EDEVICE, EINVAL, ENOMEM, ESCRATCH, ELAUNCH, EOVERLAP, FORMATS, MAX_R, OK, QUANTIZE_MAX_R,
@@ -83,16 +82,7 @@ def gemm_mxfp4(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, lora
                    out, stream, dtype)
 
 
-_BLOCK = {"nvfp4": 16, "mxfp4": 32, "mxfp4_few": 32}
-
-
-def gemm_mxfp4_few(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, lora_up=None,
-                   out=None, stream=None, dtype=None):
-    """Enqueue the fused MXFP4 operator for few rows (M <= FEW_MAX_M): arguments
-    and result as gemm_mxfp4, in a kernel that streams the weights once.
-    """
-    return _launch("mxfp4_few", act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up,
-                   out, stream, dtype)
+_BLOCK = {"nvfp4": 16, "mxfp4": 32}
 
 
 def _launch(fmt, act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out, stream,
@@ -141,9 +131,7 @@ def _launch(fmt, act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     with torch.cuda.device(device):
         f16 = dtype == torch.float16
-        if fmt == "mxfp4_few":
-            call = functools.partial(gemm_mxfp4_few_raw, f16)
-        elif fmt == "nvfp4":
+        if fmt == "nvfp4":
             call = gemm_w4a4_f16_raw if f16 else gemm_w4a4_raw
         else:
             call = gemm_mxfp4_f16_raw if f16 else gemm_mxfp4_raw
@@ -193,52 +181,72 @@ def quantize_w4a4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=Non
     return act, ascales, (lora_act_in if R else None)
 
 
-_HALF = None
+# ---------------------------------------------------------------- operators around the layers
+#
+# Their small calls are bound by this binding, not by the GPU, so it does each
+# check once, on plain attributes, and takes the stream's handle without making
+# a stream object (a call of four vectors through quantize_mxfp4_act went from
+# 19.5 to QV us, one vector through gemm_mxfp4_few from 15.2 to FV).
+
+_torch = None
+_HALF = {}
 
 
-def _f16(t, name):
+def _bind():
+    """torch, imported at the first call that needs it."""
+    global _torch
+    import torch
+    _HALF.update({torch.bfloat16: False, torch.float16: True})
+    _torch = torch
+    return torch
+
+
+def _half(t, name):
     """Whether a 16-bit floating tensor on a GPU is binary16 (else bfloat16)."""
-    global _HALF
-    if _HALF is None:
-        import torch
-        _HALF = {torch.bfloat16: False, torch.float16: True}
+    if _torch is None:
+        _bind()
     f16 = _HALF.get(t.dtype)
     if f16 is None:
         raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensors must live on a GPU device")
     return f16
 
 
-def _enqueue(device, stream, call, *args):
-    """call(*args, stream handle) with `device` current; raises on a nonzero code."""
-    import torch
+def _dense(t, name, dtype, shape, device):
+    """_check in the order that passes fastest."""
+    if not (t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.device == device):
+        _check(t, name, dtype, shape, device)
+
+
+def _handle(stream, index):
+    """The HIP stream of a call: `stream`, else torch's current one on that device."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == device.index:
-        rc = call(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            rc = call(*args, handle)
-    if rc != OK:
-        raise GemmError(rc)
+        return _torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _workspace(nbytes, device, stream):
-    """nbytes of device memory for a call on `stream`, and their address (None, 0: none needed).
+    """nbytes of device memory for a call on `stream` (None: torch's current one).
     The allocator hands memory out again in the order of the stream it was asked for."""
-    import torch
-    if nbytes == 0:
-        return None, 0
-    if stream is None or stream == torch.cuda.current_stream(device):
-        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    torch = _torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _call(index, fn, *args):
+    """fn(*args) with the device current; raises on a nonzero code."""
+    if _torch.cuda.current_device() == index:
+        rc = fn(*args)
     else:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        with torch.cuda.stream(stream):
-            t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return t, t.data_ptr()
+        with _torch.cuda.device(index):
+            rc = fn(*args)
+    if rc != OK:
+        raise GemmError(rc)
 
 
 def quantize_mxfp4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=None, stream=None):
@@ -248,38 +256,89 @@ def quantize_mxfp4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=No
     given, lora_act_in [M, R] = x @ lora_down^T of that type. Without lora_down
     it also lays out weights [N, K]. Outputs are allocated when None.
     Returns (act, ascales, lora_act_in or None)."""
-    import torch
-    f16 = _f16(x, "x")
-    device = x.device
+    f16 = _half(x, "x")
+    torch, device, dtype = _torch, x.device, x.dtype
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     M, K = x.shape
-    _check(x, "x", x.dtype, (M, K), device)
-    R = 0
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    R = ld = la = 0
     if lora_down is not None:
         R = lora_down.shape[0]
-        _check(lora_down, "lora_down", x.dtype, (R, K), device)
+        _dense(lora_down, "lora_down", dtype, (R, K), device)
+    u8 = torch.uint8
     if act is None:
-        act = torch.empty((M, K // 2), dtype=torch.uint8, device=device)
+        act = torch.empty((M, K // 2), dtype=u8, device=device)
     else:
-        _check(act, "act", torch.uint8, (M, K // 2), device)
+        _dense(act, "act", u8, (M, K // 2), device)
     if ascales is None:
-        ascales = torch.empty((K // 32, M), dtype=torch.uint8, device=device)
+        ascales = torch.empty((K // 32, M), dtype=u8, device=device)
     else:
-        _check(ascales, "ascales", torch.uint8, (K // 32, M), device)
+        _dense(ascales, "ascales", u8, (K // 32, M), device)
     if R > 0:
         if lora_act_in is None:
-            lora_act_in = torch.empty((M, R), dtype=x.dtype, device=device)
+            lora_act_in = torch.empty((M, R), dtype=dtype, device=device)
         else:
-            _check(lora_act_in, "lora_act_in", x.dtype, (M, R), device)
-    with torch.cuda.device(device):
-        nbytes = _native.load().quantize_mxfp4_workspace(M, K, R)
-    if nbytes < 0:
-        raise GemmError(nbytes)
-    keep, ws = _workspace(nbytes, device, stream)
-    _enqueue(device, stream, quantize_mxfp4_raw, f16, x.data_ptr(), lora_down.data_ptr() if R else 0,
-             act.data_ptr(), ascales.data_ptr(), lora_act_in.data_ptr() if R else 0, M, K, R, ws, nbytes)
+            _dense(lora_act_in, "lora_act_in", dtype, (M, R), device)
+        ld, la = lora_down.data_ptr(), lora_act_in.data_ptr()
+    lib, index = _native.load(), device.index
+    need = lib.quantize_mxfp4_workspace(M, K, R)
+    ws = _workspace(need, device, stream) if need > 0 else None
+    _call(index, lib.quantize_mxfp4_act_f16 if f16 else lib.quantize_mxfp4_act, x.data_ptr(), ld, act.data_ptr(),
+          ascales.data_ptr(), la, M, K, R, 0 if ws is None else ws.data_ptr(), need, _handle(stream, index))
     return act, ascales, (lora_act_in if R else None)
+
+
+def gemm_mxfp4_few(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, lora_up=None,
+                   out=None, stream=None, dtype=None):
+    """Enqueue the fused MXFP4 operator for few rows (M <= FEW_MAX_M): arguments
+    and result as gemm_mxfp4, in a kernel that streams the weights once.
+    """
+    if dtype is None:
+        given = out if out is not None else lora_act_in
+        if given is not None:
+            dtype = given.dtype
+    torch = _torch or _bind()
+    if dtype is None:
+        dtype = torch.bfloat16
+    f16 = _HALF.get(dtype)
+    if f16 is None:
+        raise TypeError(f"the LoRA/output type must be bfloat16 or float16, got {dtype}")
+    if not act.is_cuda:
+        raise ValueError("tensors must live on a GPU device")
+    if act.dim() != 2 or wgt.dim() != 2:
+        raise ValueError("act and wgt must be 2-D")
+    device, u8, f32 = act.device, torch.uint8, torch.float32
+    M, half = act.shape
+    N = wgt.shape[0]
+    if ascales.dtype != u8 and ascales.dtype == getattr(torch, "float8_e8m0fnu", None):
+        ascales = ascales.view(u8)
+    if wscales.dtype != u8 and wscales.dtype == getattr(torch, "float8_e8m0fnu", None):
+        wscales = wscales.view(u8)
+    _dense(act, "act", u8, (M, half), device)
+    _dense(wgt, "wgt", u8, (N, half), device)
+    _dense(ascales, "ascales", u8, (half // 16, M), device)
+    _dense(wscales, "wscales", u8, (half // 16, N), device)
+    _dense(wcscale, "wcscale", f32, (N,), device)
+    _dense(bias, "bias", f32, (N,), device)
+    if (lora_act_in is None) != (lora_up is None):
+        raise ValueError("lora_act_in and lora_up go together")
+    R = la = lu = 0
+    if lora_act_in is not None:
+        R = lora_act_in.shape[1]
+        _dense(lora_act_in, "lora_act_in", dtype, (M, R), device)
+        _dense(lora_up, "lora_up", dtype, (R, N), device)
+        la, lu = lora_act_in.data_ptr(), lora_up.data_ptr()
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=device)
+    else:
+        _dense(out, "out", dtype, (M, N), device)
+    lib, index = _native.load(), device.index
+    _call(index, lib.gemm_mxfp4_few_f16 if f16 else lib.gemm_mxfp4_few, act.data_ptr(), ascales.data_ptr(),
+          wgt.data_ptr(), wscales.data_ptr(), wcscale.data_ptr(), bias.data_ptr(), la, lu, out.data_ptr(),
+          M, N, 2 * half, R, _handle(stream, index))
+    return out
 
 
 def rotary_axes(x, positions, inv_freq, sections, interleaved=True, inverse=False, out=None, stream=None):
@@ -295,37 +354,41 @@ def rotary_axes(x, positions, inv_freq, sections, interleaved=True, inverse=Fals
     of x from the gradient of the result. out: allocated (dense) when None; x
     itself for in place. Returns out.
     """
-    import torch
-    f16 = _f16(x, "x")
-    device = x.device
+    f16 = _half(x, "x")
+    torch, device = _torch, x.device
     if x.dim() != 4:
         raise ValueError("x must be [batch, tokens, heads, head_dim]")
-    B, L, H, D = x.shape
-    axes = len(sections)
+    shape = x.shape
+    B, L, H, D = shape
+    axes, pairs = len(sections), sum(sections)
     if not 1 <= axes <= ROTARY_MAX_AXES:
         raise ValueError(f"1 to {ROTARY_MAX_AXES} axes, got {axes}")
     if positions.dtype != torch.int32 or inv_freq.dtype != torch.float32:
         raise TypeError("positions must be int32 and inv_freq float32")
-    if tuple(positions.shape) not in ((B, L, axes), (L, axes)):
+    ps = positions.stride()
+    if positions.shape == (B, L, axes):
+        pb, pl = ps[0], ps[1]
+    elif positions.shape == (L, axes):
+        pb, pl = 0, ps[0]
+    else:
         raise ValueError(f"positions must be [{B}, {L}, {axes}] or [{L}, {axes}], got {tuple(positions.shape)}")
-    if tuple(inv_freq.shape) != (sum(sections),) or not inv_freq.is_contiguous():
+    if inv_freq.shape != (pairs,) or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be contiguous, one value per pair")
     if positions.device != device or inv_freq.device != device:
         raise ValueError(f"positions and inv_freq must be on {device}")
-    if axes > 1 and positions.stride(-1) != 1 or x.stride(3) != 1 and D > 1:
-        raise ValueError("the last dimension of x and of positions must be dense")
+    xb, xl, xh, xd = x.stride()
     if out is None:
-        out = torch.empty((B, L, H, D), dtype=x.dtype, device=device)
-    else:
-        if out.dtype != x.dtype or out.shape != x.shape or out.device != device:
-            raise ValueError("out must have x's type, shape and device")
-        if out.stride(3) != 1 and D > 1:
-            raise ValueError("the last dimension of out must be dense")
-    ps = positions.stride()
-    args = RotaryArgs(x.data_ptr(), out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), B, L, H, D, axes,
-                      tuple(sections), x.stride()[:3], out.stride()[:3], ps[:2] if len(ps) == 3 else (0, ps[0]),
-                      bool(interleaved), bool(inverse), f16)
-    _enqueue(device, stream, rotary_axes_raw, args)
+        out = torch.empty(shape, dtype=x.dtype, device=device)
+    elif out.dtype != x.dtype or out.shape != shape or out.device != device:
+        raise ValueError("out must have x's type, shape and device")
+    ob, ol, oh, od = out.stride()
+    if (axes > 1 and ps[-1] != 1) or (D > 1 and (xd != 1 or od != 1)):
+        raise ValueError("the last dimension of x, out and positions must be dense")
+    args = ROTARY_PACK(x.data_ptr(), out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), B, L, H, D, axes,
+                       *sections, *(0,) * (ROTARY_MAX_AXES - axes), xb, xl, xh, ob, ol, oh, pb, pl,
+                       bool(interleaved), bool(inverse), f16)
+    index = device.index
+    _call(index, _native.load().rotary_axes, args, _handle(stream, index))
     return out
 
 
@@ -342,37 +405,45 @@ def cross_attention(q, k, v, kv_lens=None, scale=None, return_lse=False, out=Non
     dense when None), and with return_lse also the float32 log-sum-exp
     [batch, q_heads, q_len] (-inf for rows without keys).
     """
-    import torch
-    f16 = _f16(q, "q")
-    device = q.device
+    f16 = _half(q, "q")
+    torch, device, dtype = _torch, q.device, q.dtype
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k and v must be 4-D")
-    B, LQ, HQ, D = q.shape
-    LK, HKV = k.shape[1], k.shape[2]
-    for t, name, shape in ((k, "k", (B, LK, HKV, D)), (v, "v", (B, LK, HKV, D))):
-        if t.dtype != q.dtype:
-            raise TypeError(f"{name} must be {q.dtype}, got {t.dtype}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    shape, kshape = q.shape, k.shape
+    B, LQ, HQ, D = shape
+    LK, HKV = kshape[1], kshape[2]
+    if kshape[0] != B or kshape[3] != D or v.shape != kshape:
+        raise ValueError(f"k and v must be [{B}, kv_len, kv_heads, {D}], got {tuple(kshape)} and {tuple(v.shape)}")
+    if k.dtype != dtype or v.dtype != dtype:
+        raise TypeError(f"k and v must be {dtype}, got {k.dtype} and {v.dtype}")
+    if k.device != device or v.device != device:
+        raise ValueError(f"k and v must be on {device}")
+    lens = l = 0
     if kv_lens is not None:
-        _check(kv_lens, "kv_lens", torch.int32, (B,), device)
+        _dense(kv_lens, "kv_lens", torch.int32, (B,), device)
+        lens = kv_lens.data_ptr()
     if out is None:
-        out = torch.empty((B, LQ, HQ, D), dtype=q.dtype, device=device)
-    elif out.dtype != q.dtype or out.shape != q.shape or out.device != device:
+        out = torch.empty(shape, dtype=dtype, device=device)
+    elif out.dtype != dtype or out.shape != shape or out.device != device:
         raise ValueError("out must have q's type, shape and device")
-    for t in (q, k, v, out):
-        if t.stride(3) != 1 and D > 1:
-            raise ValueError("the last dimension of q, k, v and out must be dense")
-    lse = torch.empty((B, HQ, LQ), dtype=torch.float32, device=device) if return_lse else None
-    args = AttentionArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0,
-                         kv_lens.data_ptr() if kv_lens is not None else 0, B, LQ, LK, HQ, HKV, D, q.stride()[:3],
-                         k.stride()[:3], v.stride()[:3], out.stride()[:3], D ** -0.5 if scale is None else scale, f16)
-    nbytes = cross_attention_workspace(args)
-    if nbytes < 0:
-        raise GemmError(nbytes)
-    keep, ws = _workspace(nbytes, device, stream)
-    args.workspace, args.workspace_bytes = ws, nbytes
-    _enqueue(device, stream, cross_attention_raw, args)
+    lse = None
+    if return_lse:
+        lse = torch.empty((B, HQ, LQ), dtype=torch.float32, device=device)
+        l = lse.data_ptr()
+    qb, ql, qh, qd = q.stride()
+    kb, kl, kh, kd = k.stride()
+    vb, vl, vh, vd = v.stride()
+    ob, ol, oh, od = out.stride()
+    if D > 1 and not qd == kd == vd == od == 1:
+        raise ValueError("the last dimension of q, k, v and out must be dense")
+    if scale is None:
+        scale = D ** -0.5
+    lib, index = _native.load(), device.index
+    rest = (B, LQ, LK, HQ, HKV, D, qb, ql, qh, kb, kl, kh, vb, vl, vh, ob, ol, oh, scale, f16)
+    args = ATTENTION_PACK(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), l, lens, *rest, 0, 0)
+    need = lib.cross_attention_workspace(args)
+    if need > 0:
+        ws = _workspace(need, device, stream)
+        args = ATTENTION_PACK(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), l, lens, *rest, ws.data_ptr(), need)
+    _call(index, lib.cross_attention, args, _handle(stream, index))
     return (out, lse) if return_lse else out

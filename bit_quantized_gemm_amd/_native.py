@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from .build import LIB_PATH
@@ -58,6 +59,12 @@ class AttentionArgs(ctypes.Structure):
                [(f, ctypes.c_int64 * 3) for f in ("q_stride", "k_stride", "v_stride", "out_stride")] + \
                [("scale", ctypes.c_float), ("f16", ctypes.c_int), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_int64)]
+
+
+# The same structures as bytes in one step (building a ctypes one costs a
+# microsecond more), in the order of their fields, "x" where a C compiler pads.
+ROTARY_PACK = struct.Struct("4P9i4x8q3i4x").pack
+ATTENTION_PACK = struct.Struct("6P6i12qfiPq").pack
 
 
 class Plan(ctypes.Structure):
@@ -125,11 +132,11 @@ def load() -> ctypes.CDLL:
         for name in ("gemm_mxfp4_few", "gemm_mxfp4_few_f16"):
             getattr(lib, name).argtypes = [vp] * 9 + [i, i, i, i, vp]
             getattr(lib, name).restype = i
-        lib.rotary_axes.argtypes = [ctypes.POINTER(RotaryArgs), vp]
+        lib.rotary_axes.argtypes = [vp, vp]
         lib.rotary_axes.restype = i
-        lib.cross_attention.argtypes = [ctypes.POINTER(AttentionArgs), vp]
+        lib.cross_attention.argtypes = [vp, vp]
         lib.cross_attention.restype = i
-        lib.cross_attention_workspace.argtypes = [ctypes.POINTER(AttentionArgs)]
+        lib.cross_attention_workspace.argtypes = [vp]
         lib.cross_attention_workspace.restype = i64
         lib.gemm_w4a4_strerror.argtypes = [i]
         lib.gemm_w4a4_strerror.restype = ctypes.c_char_p
