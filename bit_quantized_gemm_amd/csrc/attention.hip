@@ -18,13 +18,14 @@
 // K and V go to LDS by direct-to-LDS buffer loads, two stages of KT keys. The
 // descriptors end with the sequence's last key, so keys past kv_lens and the
 // padding of head sizes to DP read as zeros, whatever memory holds there.
-// 16-byte chunks are XOR-swizzled by row (K: chunk ^ row, for reads of 32 rows
-// at one chunk; V: chunk ^ 2 row, for transposed reads of 8 rows at two).
+// 16-byte chunks are XOR-swizzled by row so that no read meets a bank twice (K:
+// reads of 16 rows at one chunk; V: transposing reads of 4 rows at four).
 //
 // Rows of a (sequence, key head) are (token, query head of the group) pairs, so
 // heads that share keys share a tile. Few rows: the waves of a workgroup take
-// different keys for the same 32 rows and join in LDS, and the keys are split
-// over workgroups whose parts a second launch joins, in order.
+// different keys for the same 32 rows and join in LDS, and the keys of
+// tiles that would fill no round of the compute units are cut into parts, a
+// workgroup each, which a second launch joins, in order.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -47,16 +48,49 @@ struct AttnParams {
   uint16_t* out;
   float* lse;
   const int32_t* kv_lens;
-  float* part_o;       // splits > 1: [split][pair][row][D] sums, then
-  float* part_ms;      //             [split][pair][row][2] maximum (log2 units) and sum
+  float* part_o;       // the cut tiles' [tile][part][row of the tile][D] sums and
+  float* part_ms;      // [tile][part][row of the tile][2] maximum (log2 units) and sum
   int64_t qs[3], ks[3], vs[3], os[3];   // batch, token, head
   int q_len, kv_len, kv_heads, D, group;   // group: query heads of a key head
   int rows;            // q_len * group
-  int tiles;           // row tiles of a (sequence, key head) pair
   int pairs;           // batch * kv_heads
-  int splits;
+  int whole;           // the first tiles are done whole; the keys of the cut tiles
+  int cut, parts;      // after them in so many parts, a workgroup each
   float c;             // scale * log2(e)
 };
+
+// What a workgroup does: keys first .. first + len - 1 for row tile `tile` of
+// (sequence, key head) `pair`. KT: keys are divided in multiples of it.
+struct Share {
+  int pair, tile, b, kvh;
+  int first, len;
+  int slot;            // of a cut tile: (tile, part) in the workspace; else -1
+};
+
+template <int KT>
+__device__ __forceinline__ Share share_of(const AttnParams& p) {
+  Share w;
+  const int idx = blockIdx.x;
+  const bool cut = idx >= p.whole;
+  const int part = cut ? (idx - p.whole) / p.cut : 0, nth = cut ? (idx - p.whole) % p.cut : 0;
+  const int id = cut ? p.whole + nth : idx;
+  w.slot = cut ? nth * p.parts + part : -1;
+  w.pair = id % p.pairs;
+  w.tile = id / p.pairs;
+  w.b = w.pair / p.kv_heads;
+  w.kvh = w.pair - w.b * p.kv_heads;
+  int len = p.kv_len;
+  if (p.kv_lens) len = min(max(p.kv_lens[w.b], 0), p.kv_len);
+  len = __builtin_amdgcn_readfirstlane(len);
+  w.first = 0;
+  w.len = len;
+  if (cut) {
+    const int64_t all = (len + KT - 1) / KT;
+    w.first = int(all * part / p.parts) * KT;
+    w.len = max(0, min(len, int(all * (part + 1) / p.parts) * KT) - w.first);
+  }
+  return w;
+}
 
 // WQ waves over query rows (32 each), WK waves over the keys of a stage; DP:
 // head size padded to 64, 96 or 128.
@@ -81,7 +115,7 @@ struct AttnCfg {
 template <class C>
 __device__ __forceinline__ int k_chunk(int r, int c) { return c ^ (C::CH == 16 ? r & 15 : (r >> 1) & 7); }
 template <class C>
-__device__ __forceinline__ int v_chunk(int r, int c) { return c ^ (C::CH == 16 ? (r & 7) << 1 : ((r >> 1) & 3) << 1); }
+__device__ __forceinline__ int v_chunk(int r, int c) { return c ^ (C::CH == 16 ? (r & 3) << 2 : ((r >> 1) & 1) << 2); }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -102,7 +136,46 @@ __device__ __forceinline__ float other_sum(float v) {
   return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
 }
 
-template <bool F16, class C, bool SPLIT>
+// A row's result from its sums o (values 8 (i / 4) + 4 h + i % 4 of each 32),
+// maximum m and sum l, or its part of them. r: the row in its tile.
+template <bool F16, class C>
+__device__ __forceinline__ void store_row(const AttnParams& p, const f32x16 (&o)[C::DP / 32], float m, float l,
+                                          const Share& w, int r, int tok, int hq, int h) {
+  constexpr int DT = C::DP / 32;
+  const int D = p.D;
+  if (w.slot >= 0) {
+    const int64_t at = int64_t(w.slot) * C::ROWS + r;
+    float* po = p.part_o + at * D;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int e = 32 * d + 2 * i + 4 * h;
+        if (e < D) *reinterpret_cast<f32x4*>(po + e) = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+      }
+    if (h == 0) {
+      p.part_ms[at * 2] = m;
+      p.part_ms[at * 2 + 1] = l;
+    }
+    return;
+  }
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // a NaN sum stays one
+  uint16_t* out = p.out + int64_t(w.b) * p.os[0] + int64_t(tok) * p.os[1] + int64_t(hq) * p.os[2];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int e = 32 * d + 2 * i + 4 * h;
+      if (e < D)
+        *reinterpret_cast<u32x2*>(out + e) = u32x2{narrow2<F16>(o[d][i] * inv, o[d][i + 1] * inv),
+                                                   narrow2<F16>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+    }
+  if (p.lse && h == 0)
+    p.lse[(int64_t(w.b) * p.kv_heads * p.group + hq) * p.q_len + tok] =
+        l == 0.f ? -INFINITY : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+}
+
+template <bool F16, class C>
 __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
   constexpr int DK = C::DP / 16, DT = C::DP / 32;
@@ -111,20 +184,12 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams 
   const int wq = wave % C::WQ, wk = wave / C::WQ;
   const int l32 = lane & 31, h = lane >> 5;
 
-  const int pair = blockIdx.x % p.pairs;
-  const int tile = blockIdx.x / p.pairs % p.tiles;
-  const int split = SPLIT ? blockIdx.x / p.pairs / p.tiles : 0;
-  const int b = pair / p.kv_heads, kvh = pair - b * p.kv_heads;
-  const int D = p.D;
-  int len = p.kv_len;
-  if (p.kv_lens) len = min(max(p.kv_lens[b], 0), p.kv_len);
-  len = __builtin_amdgcn_readfirstlane(len);
+  const Share w = share_of<C::KT>(p);
+  const int b = w.b, kvh = w.kvh, len = w.len, D = p.D;
   const int nt = (len + C::KT - 1) / C::KT;
-  const int t0 = SPLIT ? int(int64_t(nt) * split / p.splits) : 0;
-  const int t1 = SPLIT ? int(int64_t(nt) * (split + 1) / p.splits) : nt;
 
   // this lane's query row
-  const int row = tile * C::ROWS + wq * 32 + l32;
+  const int row = w.tile * C::ROWS + wq * 32 + l32;
   const int rowc = min(row, p.rows - 1);
   const int tok = rowc / p.group, hq = kvh * p.group + rowc % p.group;
   u32x4 qv[DK];
@@ -146,18 +211,19 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams 
   const bool klive = kc * 8 < D, vlive = vc * 8 < D;
   const uint32_t koff = klive ? uint32_t(dr) * kst + uint32_t(kc) * 16u : 0xFFFFFFF0u, kstep = klive ? C::RPR * kst : 0u;
   const uint32_t voff = vlive ? uint32_t(dr) * vst + uint32_t(vc) * 16u : 0xFFFFFFF0u, vstep = vlive ? C::RPR * vst : 0u;
-  const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k + int64_t(b) * p.ks[0] + int64_t(kvh) * p.ks[2]);
-  const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v + int64_t(b) * p.vs[0] + int64_t(kvh) * p.vs[2]);
+  const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k + int64_t(b) * p.ks[0] + int64_t(kvh) * p.ks[2] + int64_t(w.first) * p.ks[1]);
+  const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v + int64_t(b) * p.vs[0] + int64_t(kvh) * p.vs[2] + int64_t(w.first) * p.vs[1]);
+  const uint32_t lds0 = lds_address(smem) + wave * 1024;
   auto load_stage = [&](int t) __attribute__((always_inline)) {
-    uint8_t* dst = smem + (t & 1) * 2 * C::TILE + wave * 1024;
+    const uint32_t dst = lds0 + (t & 1) * 2 * C::TILE;
     // (rows - 1) strides and one row: below 2^31, strides are below 2^24 bytes
     const int rows = min(len - t * C::KT, C::KT);
-    const __amdgpu_buffer_rsrc_t kr = row_rsrc(kb + int64_t(t * C::KT) * kst, uint32_t(rows - 1) * kst + uint32_t(D) * 2u);
-    const __amdgpu_buffer_rsrc_t vr = row_rsrc(vb + int64_t(t * C::KT) * vst, uint32_t(rows - 1) * vst + uint32_t(D) * 2u);
+    const u32x4 kr = range_desc(kb + int64_t(t * C::KT) * kst, uint32_t(rows - 1) * kst + uint32_t(D) * 2u);
+    const u32x4 vr = range_desc(vb + int64_t(t * C::KT) * vst, uint32_t(rows - 1) * vst + uint32_t(D) * 2u);
 #pragma unroll
     for (int u = 0; u < C::ROUNDS; ++u) {
-      dma_rows(kr, koff + u * kstep, dst + u * C::RPR * C::ROWB);
-      dma_rows(vr, voff + u * vstep, dst + u * C::RPR * C::ROWB + C::TILE);
+      load_to_lds(kr, koff + u * kstep, dst + u * C::RPR * C::ROWB);
+      load_to_lds(vr, voff + u * vstep, dst + u * C::RPR * C::ROWB + C::TILE);
     }
   };
 
@@ -173,11 +239,11 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams 
   const int vr = (lane & 15) >> 2;                       // row of the four
   const int vcol = 4 * ((lane >> 4) & 1) + (lane & 3);   // run of 4 values among the 32 of a d tile
 
-  if (t0 < t1) load_stage(t0);
-  for (int t = t0; t < t1; ++t) {
+  if (nt > 0) load_stage(0);
+  for (int t = 0; t < nt; ++t) {
     wait_vm_lgkm0<0>();
     __syncthreads();
-    if (t + 1 < t1) load_stage(t + 1);
+    if (t + 1 < nt) load_stage(t + 1);
     const uint8_t* st = smem + (t & 1) * 2 * C::TILE;
 
     f32x16 sc[C::NKT];
@@ -260,7 +326,7 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams 
     if (wk != 0) return;
     float mm = m;
 #pragma unroll
-    for (int w = 1; w < C::WK; ++w) mm = fmaxf(mm, mg[(w * 32 + l32) * S + C::DP]);
+    for (int v = 1; v < C::WK; ++v) mm = fmaxf(mm, mg[(v * 32 + l32) * S + C::DP]);
     const float ms = mm == -INFINITY ? 0.f : mm;
     const float f0 = __builtin_amdgcn_exp2f(m - ms);
     l *= f0;
@@ -269,8 +335,8 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams 
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][i] *= f0;
 #pragma unroll
-    for (int w = 1; w < C::WK; ++w) {
-      const float* other = mg + (w * 32 + l32) * S;
+    for (int v = 1; v < C::WK; ++v) {
+      const float* other = mg + (v * 32 + l32) * S;
       const float f = __builtin_amdgcn_exp2f(other[C::DP] - ms);
       l += other[C::DP + 1] * f;
 #pragma unroll
@@ -286,58 +352,294 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams 
   }
 
   if (row >= p.rows) return;
-  if constexpr (SPLIT) {
-    const int64_t at = (int64_t(split) * p.pairs + pair) * p.rows + row;
-    float* po = p.part_o + at * D;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int e = 32 * d + 2 * i + 4 * h;
-        if (e < D) *reinterpret_cast<f32x4*>(po + e) = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
-      }
-    if (h == 0) {
-      p.part_ms[at * 2] = m;
-      p.part_ms[at * 2 + 1] = l;
-    }
-  } else {
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // a NaN sum stays one
-    uint16_t* out = p.out + int64_t(b) * p.os[0] + int64_t(tok) * p.os[1] + int64_t(hq) * p.os[2];
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int e = 32 * d + 2 * i + 4 * h;
-        if (e < D)
-          *reinterpret_cast<u32x2*>(out + e) = u32x2{narrow2<F16>(o[d][i] * inv, o[d][i + 1] * inv),
-                                                     narrow2<F16>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-      }
-    if (p.lse && h == 0)
-      p.lse[(int64_t(b) * p.kv_heads * p.group + hq) * p.q_len + tok] = l == 0.f ? -INFINITY : (m + __builtin_log2f(l)) * 0.6931471805599453f;
-  }
+  store_row<F16, C>(p, o, m, l, w, wq * 32 + l32, tok, hq, h);
 }
 
-// Joins the splits' parts of a row, in split order: one thread per 4 values.
+// ------------------------------------------------------------------ many rows
+//
+// 32 rows a wave, 4 waves a workgroup, two workgroups a compute unit, and each
+// wave's own instructions overlapped: step j runs, all independent of each
+// other, the score MFMAs of the 32 keys j + 1, the softmax of the 32 keys j on
+// the vector ALU and the product MFMAs of the 32 keys j - 1. The step is
+// written out MFMA by MFMA (products and scores in turn), each with its share
+// of the softmax and of the operand reads of four MFMAs on, fenced so that the
+// order stays.
+//
+// K and V pass through registers on their way to LDS, asked for two steps
+// before they are put there (the compiler waits for every direct-to-LDS load
+// before any transposing read). Rings of four 32-key tiles each, one meeting
+// of the workgroup a step, in its middle.
+//
+// The sums are rescaled only when a row's maximum has grown by more than
+// kSlack (in powers of two) past the one its weights are taken against; until
+// then weights are at most 2^kSlack, which float32 sums and the 16-bit types
+// hold without loss.
+constexpr float kSlack = 8.f;
+
+template <int DP_>
+struct WideAttn {
+  static constexpr int DP = DP_, WAVES = 4, KT = 32, RING = 4;
+  static constexpr int THREADS = WAVES * kWave;
+  static constexpr int ROWS = WAVES * 32;
+  static constexpr int ROWB = DP > 64 ? 256 : 128;
+  static constexpr int CH = ROWB / 16;
+  static constexpr int TILE = KT * ROWB;
+  static constexpr int RPR = THREADS * 16 / ROWB;   // rows a round of loads covers
+  static constexpr int ROUNDS = KT / RPR;           // rounds of a tile
+  static constexpr int LDS = 2 * RING * TILE;       // K tiles, then V tiles
+  static_assert(KT % RPR == 0 && ROUNDS >= 1 && RPR % 16 == 0, "whole rounds; the swizzles repeat every 16 rows");
+  static_assert(2 * LDS <= kLdsLimit, "two workgroups a compute unit");
+};
+
+template <bool F16, class C>
+__global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const AttnParams p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
+  constexpr int DK = C::DP / 16, DT = C::DP / 32, VOFF = C::RING * C::TILE;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  // Two workgroups share a compute unit; the second of them (256 on) goes first
+  // where both can issue, so that the two do not run in step and wait for the
+  // same units (4352 x 4608 keys, 24 heads of 128: 265 to 256 us).
+  if (blockIdx.x & 256) __builtin_amdgcn_s_setprio(2);
+  const Share w = share_of<C::KT>(p);
+  const int b = w.b, kvh = w.kvh, len = w.len, D = p.D;
+  const int n = (len + C::KT - 1) / C::KT;
+
+  const int row = w.tile * C::ROWS + wave * 32 + l32;
+  const int rowc = min(row, p.rows - 1);
+  const int tok = rowc / p.group, hq = kvh * p.group + rowc % p.group;
+  u32x4 qv[DK];
+  {
+    const uint16_t* q = p.q + int64_t(b) * p.qs[0] + int64_t(tok) * p.qs[1] + int64_t(hq) * p.qs[2];
+#pragma unroll
+    for (int s = 0; s < DK; ++s) {
+      const int d = 16 * s + 8 * h;
+      qv[s] = d < D ? *reinterpret_cast<const u32x4*>(q + d) : u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+
+  // loads: round u covers rows u RPR .. of a tile; lane -> (row, chunk
+  // position); chunks past D are out of every range and read zeros
+  const int dr = tid / C::CH, dp = tid % C::CH;
+  const int kc = k_chunk<C>(dr, dp), vc = v_chunk<C>(dr, dp);
+  const uint32_t kst = uint32_t(p.ks[1]) * 2u, vst = uint32_t(p.vs[1]) * 2u;
+  const bool klive = kc * 8 < D, vlive = vc * 8 < D;
+  const uint32_t koff = klive ? uint32_t(dr) * kst + uint32_t(kc) * 16u : 0xFFFFFFF0u, kstep = klive ? C::RPR * kst : 0u;
+  const uint32_t voff = vlive ? uint32_t(dr) * vst + uint32_t(vc) * 16u : 0xFFFFFFF0u, vstep = vlive ? C::RPR * vst : 0u;
+  const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k + int64_t(b) * p.ks[0] + int64_t(kvh) * p.ks[2] + int64_t(w.first) * p.ks[1]);
+  const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v + int64_t(b) * p.vs[0] + int64_t(kvh) * p.vs[2] + int64_t(w.first) * p.vs[1]);
+  const uint32_t lds0 = lds_address(smem) + wave * 1024;
+  // Tile t of K (to ring place t % RING) or V; tiles past the last key are
+  // empty ranges: zeros (by a mask and no branch, so that a step stays one block).
+  auto load = [&](const uint8_t* base, uint32_t stride, uint32_t off, uint32_t step, int t, uint32_t to) __attribute__((always_inline)) {
+    const int rows = min(len - t * C::KT, C::KT);
+    const uint32_t any = uint32_t(-rows >> 31);   // all ones where rows > 0
+    const u32x4 rs = range_desc(base + int64_t(t * C::KT) * stride, (uint32_t(rows - 1) * stride + uint32_t(D) * 2u) & any);
+#pragma unroll
+    for (int u = 0; u < C::ROUNDS; ++u) load_to_lds(rs, off + u * step, lds0 + to + u * C::RPR * C::ROWB);
+  };
+  auto load_k = [&](int t, int ring) __attribute__((always_inline)) { load(kb, kst, koff, kstep, t, ring * C::TILE); };
+  auto load_v = [&](int t, int ring) __attribute__((always_inline)) { load(vb, vst, voff, vstep, t, VOFF + ring * C::TILE); };
+
+  // this lane's LDS addresses in the rings' first tiles, by slot
+  uint32_t kaddr[DK], vaddr[DT];
+#pragma unroll
+  for (int i = 0; i < DK; ++i) kaddr[i] = l32 * C::ROWB + k_chunk<C>(l32, 2 * i + h) * 16;
+#pragma unroll
+  for (int d = 0; d < DT; ++d) {
+    const int r = 4 * h + ((lane & 15) >> 2), run = 8 * d + 4 * ((lane >> 4) & 1) + (lane & 3);
+    vaddr[d] = VOFF + r * C::ROWB + v_chunk<C>(r, run >> 1) * 16 + (run & 1) * 8;
+  }
+  // K operand of score slot i (16 of D); V operand of product slot i: 16 keys
+  // i / DT, 32 of D i % DT
+  auto read_k = [&](int ring, int i) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u32x4*>(smem + kaddr[i] + ring * C::TILE);
+  };
+  auto read_v = [&](int ring, int i) __attribute__((always_inline)) {
+    const uint8_t* v = smem + vaddr[i % DT] + (ring * C::TILE + i / DT * 16 * C::ROWB);
+    const u32x2 lo = read_transposed(v), hi = read_transposed(v + 8 * C::ROWB);
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+  };
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  f32x16 sc[2];         // scores, by key tile's parity
+  u32x4 pv[2][2];       // weights, likewise
+  u32x4 ka[2], va[2];   // operands of the next two score and product slots
+
+  // The softmax of a step in parts: the maximum by quarters and what follows
+  // from it, then the weights one key at a time.
+  constexpr int FIN = 8, PARTS = FIN + 16;
+  float alpha, ms, top, grown, drop, e[4];
+  auto soft = [&]<bool TAIL>(int part, f32x16& s, u32x4 (&wt)[2], int key0) __attribute__((always_inline)) {
+    if (part < 4) {
+      if constexpr (TAIL) {
+#pragma unroll
+        for (int i = 4 * part; i < 4 * part + 4; ++i)
+          if (key0 + 8 * (i >> 2) + 4 * h + (i & 3) >= len) s[i] = -INFINITY;
+      }
+      float t = part == 0 ? s[0] : top;
+#pragma unroll
+      for (int i = 4 * part; i < 4 * part + 4; ++i) t = fmaxf(t, s[i]);
+      top = t;
+    } else if (part == 4) {
+      top = other_max(top);
+    } else if (part == 5) {
+      // the maximum in use grows, or stays and alpha, the factor of what was
+      // summed before, is 1 (the first keys: m is -inf)
+      top *= p.c;
+      grown = top > m + kSlack ? top : m;
+    } else if (part == 6) {
+      drop = m == grown ? 0.f : m - grown;
+      ms = grown == -INFINITY ? 0.f : grown;
+      m = grown;
+    } else if (part == 7) {
+      alpha = __builtin_amdgcn_exp2f(drop);
+      l *= alpha;
+    } else {
+      // an exponential is used one part after it was asked for
+      const int i = part - FIN;
+      if (i > 0) l += e[(i - 1) & 3];
+      if (i > 0 && i % 2 == 0) wt[(i - 2) >> 3][((i - 2) >> 1) & 3] = narrow2<F16>(e[(i - 2) & 3], e[(i - 1) & 3]);
+      e[i & 3] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.c, -ms));
+      if (i == 15) {
+        l += e[3];
+        wt[1][3] = narrow2<F16>(e[2], e[3]);
+      }
+    }
+  };
+  // Where each part goes: in proportion to cycles, counting the latency of
+  // chained instructions, after a lead in which the last scores come in.
+  constexpr int kLead = 40, kMaxCost = 20, kFinCost = 28, kKeyCost = 18, MFMAS = 2 * DK;
+  constexpr auto cost_before = [](int part) {
+    int c = kLead;
+    for (int i = 0; i < part; ++i) c += i < 4 ? kMaxCost : i < FIN ? kFinCost : kKeyCost;
+    return c;
+  };
+  constexpr auto first_part = [=](int mfma) {   // the first part at or after MFMA `mfma`'s share
+    int i = 0;
+    while (i < PARTS && cost_before(i) * MFMAS < cost_before(PARTS) * mfma) ++i;
+    return i;
+  };
+  // Step j; R: j % RING. Reads K tile j + 1 and V tile j - 1 and, at its end,
+  // the first operands of step j + 1 (K tile j + 2, V tile j). In its second
+  // half, K tile j + 3 and V tile j + 1 go to LDS, over K tile j - 1 and V tile
+  // j - 3, last read in step j - 2 (before every wave met in step j - 1); they
+  // are published by the meeting of step j + 1, and first read after it.
+  auto step = [&]<bool TAIL, int R>(int j) __attribute__((always_inline)) {
+    constexpr int P = R & 1;
+    static_for<0, MFMAS>([&]<int I>() __attribute__((always_inline)) {
+      constexpr int i = I / 2;
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (I == MFMAS / 2) {
+        wait_vm<2 * C::ROUNDS>();
+        wg_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (I % 2 == 0) {
+        o[i % DT] = mfma32<F16>(va[i % 2], pv[1 - P][i / DT], o[i % DT]);
+        va[i % 2] = i + 2 < DK ? read_v((R + 3) & 3, i + 2) : read_v(R, i + 2 - DK);
+      } else {
+        sc[1 - P] = mfma32<F16>(ka[i % 2], qv[i], i == 0 ? f32x16{} : sc[1 - P]);
+        ka[i % 2] = i + 2 < DK ? read_k((R + 1) & 3, i + 2) : read_k((R + 2) & 3, i + 2 - DK);
+      }
+      static_for<first_part(I), first_part(I + 1)>([&]<int PART>() __attribute__((always_inline)) {
+        soft.template operator()<TAIL>(PART, sc[P], pv[P], j * C::KT);
+      });
+      if constexpr (I == MFMAS / 2) load_k(j + 4, R);
+      if constexpr (I == MFMAS / 2 + 1) load_v(j + 2, (R + 2) & 3);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+    // (the compiler would move the weights past the branch, away from the MFMAs)
+    asm volatile("" : "+v"(pv[P][0]), "+v"(pv[P][1]), "+v"(l));
+    if (__builtin_amdgcn_ballot_w64(alpha != 1.f)) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+    }
+  };
+  static_assert(C::RING == 4 && MFMAS >= 8, "the step above");
+
+  if (n > 0) {
+    // zeros stand in for the values before the first
+    for (int i = tid * 16; i < C::TILE; i += C::THREADS * 16) *reinterpret_cast<u32x4*>(smem + VOFF + 3 * C::TILE + i) = u32x4{0u, 0u, 0u, 0u};
+    load_k(0, 0);
+    load_k(1, 1);
+    load_v(0, 0);
+    load_k(2, 2);
+    load_v(1, 1);
+    load_k(3, 3);
+    wait_vm_lgkm0<4 * C::ROUNDS>();
+    wg_barrier();
+#pragma unroll
+    for (int i = 0; i < DK; ++i) sc[0] = mfma32<F16>(read_k(0, i), qv[i], i == 0 ? f32x16{} : sc[0]);
+    pv[1][0] = pv[1][1] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ka[i] = read_k(1, i);
+      va[i] = read_v(3, i);
+    }
+    const int full = len / C::KT;
+    int j = 0;
+    for (; j + 4 <= full; j += 4) {
+      step.template operator()<false, 0>(j);
+      step.template operator()<false, 1>(j + 1);
+      step.template operator()<false, 2>(j + 2);
+      step.template operator()<false, 3>(j + 3);
+    }
+    if (j < n) step.template operator()<true, 0>(j);
+    if (j + 1 < n) step.template operator()<true, 1>(j + 1);
+    if (j + 2 < n) step.template operator()<true, 2>(j + 2);
+    if (j + 3 < n) step.template operator()<true, 3>(j + 3);
+    wait_vm<0>();
+    // products of the last 32 keys
+    const int last = (n - 1) & 3;
+    const bool odd = last & 1;
+    const u32x4 w0 = odd ? pv[1][0] : pv[0][0], w1 = odd ? pv[1][1] : pv[0][1];
+#pragma unroll
+    for (int i = 0; i < DK; ++i)
+      o[i % DT] = mfma32<F16>(i < 2 ? va[i] : read_v(last, i), i / DT == 0 ? w0 : w1, o[i % DT]);
+  }
+
+  if (row >= p.rows) return;
+  l = other_sum(l);
+  store_row<F16, C>(p, o, m, l, w, wave * 32 + l32, tok, hq, h);
+}
+
+// Joins the parts of the cut tiles' rows, in order: one thread per 4 values.
+// The loads of several parts are in flight at once.
 template <bool F16>
-__global__ __launch_bounds__(256) void attention_join_kernel(const AttnParams p) {
+__global__ __launch_bounds__(256) void attention_join_kernel(const AttnParams p, int tile_rows) {
   const int per = p.D / 4;
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t all = int64_t(p.pairs) * p.rows;
-  const int64_t at = i / per;
-  if (at >= all) return;
-  const int e = int(i - at * per) * 4;
+  const int64_t line = i / per;                       // (cut tile, row of it)
+  const int nth = int(line / tile_rows), r = int(line - int64_t(nth) * tile_rows);
+  if (nth >= p.cut) return;
+  const int id = p.whole + nth, pair = id % p.pairs, row = id / p.pairs * tile_rows + r;
+  if (row >= p.rows) return;
+  const int e = int(i - line * per) * 4;
+  const int64_t at = int64_t(nth) * p.parts * tile_rows + r;
+  const float* ms = p.part_ms + at * 2;
+  const float* po = p.part_o + at * p.D + e;
   float mm = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) mm = fmaxf(mm, p.part_ms[(s * all + at) * 2]);
-  const float ms = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 8
+  for (int s = 0; s < p.parts; ++s) mm = fmaxf(mm, ms[int64_t(s) * tile_rows * 2]);
+  const float base = mm == -INFINITY ? 0.f : mm;
   float l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.splits; ++s) {
-    const float f = __builtin_amdgcn_exp2f(p.part_ms[(s * all + at) * 2] - ms);
-    l += p.part_ms[(s * all + at) * 2 + 1] * f;
-    o += *reinterpret_cast<const f32x4*>(p.part_o + (s * all + at) * p.D + e) * f;
+#pragma unroll 8
+  for (int s = 0; s < p.parts; ++s) {
+    const float f = __builtin_amdgcn_exp2f(ms[int64_t(s) * tile_rows * 2] - base);
+    l += ms[int64_t(s) * tile_rows * 2 + 1] * f;
+    o += *reinterpret_cast<const f32x4*>(po + int64_t(s) * tile_rows * p.D) * f;
   }
   const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-  const int pair = int(at / p.rows), row = int(at - int64_t(pair) * p.rows);
   const int b = pair / p.kv_heads, tok = row / p.group, hq = (pair - b * p.kv_heads) * p.group + row % p.group;
   uint16_t* out = p.out + int64_t(b) * p.os[0] + int64_t(tok) * p.os[1] + int64_t(hq) * p.os[2];
   *reinterpret_cast<u32x2*>(out + e) = u32x2{narrow2<F16>(o.x * inv, o.y * inv), narrow2<F16>(o.z * inv, o.w * inv)};
@@ -348,8 +650,10 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnParams p)
 // ------------------------------------------------------------------ host side
 
 struct AttnPlan {
-  int shape;     // 0: many rows (4 waves of 32 rows); 1: few (4 waves over the keys)
-  int rows, tiles, pairs, splits, rows_all;
+  bool few;      // 32-row tiles, waves over the keys
+  int rows, tiles, pairs, rows_all;
+  int64_t whole;
+  int cut, parts;
   int64_t o_bytes, bytes;
 };
 
@@ -362,36 +666,46 @@ static bool attn_sizes_ok(const cross_attention_t* a) {
          int64_t(a->batch) * a->q_len * a->q_heads < lim;
 }
 
+// Tiles and which of them are cut. Up to 32 rows (token, query head of the
+// group) a pair: the few-row kernel, one workgroup a compute unit; else 128-row
+// tiles, two a compute unit. Tiles that fill no whole round of the compute
+// units are cut into the parts that would fill it, of at least kMinPart keys.
 static AttnPlan attn_plan(const cross_attention_t* a) {
+  constexpr int kMinPart = 256;
   AttnPlan pl{};
   const int group = a->q_heads / a->kv_heads;
   pl.rows_all = a->q_len * group;
   pl.pairs = a->batch * a->kv_heads;
-  pl.shape = pl.rows_all <= 32 ? 1 : 0;
-  pl.rows = pl.shape == 1 ? 32 : 128;
+  pl.few = pl.rows_all <= 32;
+  pl.rows = pl.few ? 32 : 128;
   pl.tiles = (pl.rows_all + pl.rows - 1) / pl.rows;
-  const int kt = pl.shape == 1 ? 128 : 64;
-  const int64_t wgs = int64_t(pl.tiles) * pl.pairs;
-  const int nt = (a->kv_len + kt - 1) / kt;
-  int64_t s = wgs > 0 ? std::min<int64_t>(2 * kNumCUs / wgs, nt / 2) : 1;
-  pl.splits = int(std::max<int64_t>(1, std::min<int64_t>(s, 64)));
-  if (pl.splits > 1) {
-    const int64_t n = int64_t(pl.splits) * pl.pairs * pl.rows_all;
-    pl.o_bytes = n * a->head_dim * 4;
-    pl.bytes = pl.o_bytes + n * 8;
+  pl.whole = int64_t(pl.tiles) * pl.pairs;
+  pl.parts = 1;
+  const int left = int(pl.whole % kNumCUs);
+  if (left > 0) {
+    const int slots = pl.whole < kNumCUs ? 2 * kNumCUs : kNumCUs;
+    const int parts = std::min(slots / left, a->kv_len / kMinPart);
+    if (parts > 1) {
+      pl.parts = parts;
+      pl.cut = left;
+      pl.whole -= left;
+      const int64_t n = int64_t(left) * parts * pl.rows;
+      pl.o_bytes = n * a->head_dim * 4;
+      pl.bytes = pl.o_bytes + n * 8;
+    }
   }
   return pl;
 }
 
-template <bool F16, bool SPLIT>
-static const void* attention_of(int shape, int D) {
-  if (shape == 1)
-    return D <= 64 ? reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<64, 1, 4, 128>, SPLIT>)
-         : D <= 96 ? reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<96, 1, 4, 128>, SPLIT>)
-                   : reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<128, 1, 4, 128>, SPLIT>);
-  return D <= 64 ? reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<64, 4, 1, 64>, SPLIT>)
-       : D <= 96 ? reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<96, 4, 1, 64>, SPLIT>)
-                 : reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<128, 4, 1, 64>, SPLIT>);
+template <bool F16>
+static const void* attention_of(bool few, int D) {
+  if (few)
+    return D <= 64 ? reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<64, 1, 4, 128>>)
+         : D <= 96 ? reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<96, 1, 4, 128>>)
+                   : reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<128, 1, 4, 128>>);
+  return D <= 64 ? reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<64>>)
+       : D <= 96 ? reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<96>>)
+                 : reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<128>>);
 }
 
 static int attention_run(const cross_attention_t* a, void* stream) {
@@ -453,20 +767,20 @@ static int attention_run(const cross_attention_t* a, void* stream) {
   p.D = D;
   p.group = a->q_heads / a->kv_heads;
   p.rows = pl.rows_all;
-  p.tiles = pl.tiles;
   p.pairs = pl.pairs;
-  p.splits = pl.splits;
+  p.whole = int(std::min<int64_t>(pl.whole, INT32_MAX));
+  p.cut = pl.cut;
+  p.parts = pl.parts;
   p.c = a->scale * 1.4426950408889634f;
-  void* args[] = {&p};
+  int tile_rows = pl.rows;
+  void* args[] = {&p, &tile_rows};
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const bool split = pl.splits > 1;
-  const void* k = a->f16 ? (split ? attention_of<true, true>(pl.shape, D) : attention_of<true, false>(pl.shape, D))
-                         : (split ? attention_of<false, true>(pl.shape, D) : attention_of<false, false>(pl.shape, D));
-  const int64_t grid = int64_t(pl.pairs) * pl.tiles * pl.splits;
+  const int64_t grid = pl.whole + int64_t(pl.cut) * pl.parts;
   if (grid >= (int64_t(1) << 31)) return GEMM_W4A4_EINVAL;
-  hipError_t e = hipLaunchKernel(k, dim3(unsigned(grid)), dim3(256), args, 0, st);
-  if (e == hipSuccess && split) {
-    const int64_t n = int64_t(pl.pairs) * pl.rows_all * (D / 4);
+  hipError_t e = hipLaunchKernel(a->f16 ? attention_of<true>(pl.few, D) : attention_of<false>(pl.few, D),
+                                 dim3(unsigned(grid)), dim3(256), args, 0, st);
+  if (e == hipSuccess && pl.cut > 0) {
+    const int64_t n = int64_t(pl.cut) * pl.rows * (D / 4);
     e = hipLaunchKernel(a->f16 ? reinterpret_cast<const void*>(attention_join_kernel<true>)
                                : reinterpret_cast<const void*>(attention_join_kernel<false>),
                         dim3(unsigned((n + 255) / 256)), dim3(256), args, 0, st);
