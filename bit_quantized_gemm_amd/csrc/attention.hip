@@ -92,23 +92,20 @@ __device__ __forceinline__ Share share_of(const AttnParams& p) {
   return w;
 }
 
-// WQ waves over query rows (32 each), WK waves over the keys of a stage; DP:
-// head size padded to 64, 96 or 128.
-template <int DP_, int WQ_, int WK_, int KT_>
-struct AttnCfg {
-  static constexpr int DP = DP_, WQ = WQ_, WK = WK_, KT = KT_;
-  static constexpr int THREADS = WQ * WK * kWave;
-  static constexpr int ROWS = WQ * 32;
+// Few rows: DP, the head size padded to 64, 96 or 128.
+template <int DP_>
+struct FewAttn {
+  static constexpr int DP = DP_, WAVES = 4, THREADS = WAVES * kWave, ROWS = 32;
+  static constexpr int KT = 32;                            // keys of a wave's tile
   static constexpr int ROWB = DP > 64 ? 256 : 128;         // bytes of a key's row in LDS
   static constexpr int CH = ROWB / 16;                     // 16-byte chunks of a row
-  static constexpr int TILE = KT * ROWB;                   // K or V of a stage
-  static constexpr int RPR = THREADS * 16 / ROWB;          // rows a round of loads covers
-  static constexpr int ROUNDS = KT / RPR;
-  static constexpr int NKT = KT / (32 * WK);               // 32-key tiles of a wave's share
-  static constexpr int LDS = 4 * TILE;
-  static constexpr int MERGE = WK > 1 ? WK * 32 * (DP + 4) * 4 : 0;   // join of the waves' parts
-  static_assert(KT % RPR == 0 && ROUNDS >= 1 && NKT >= 1, "whole rounds and key tiles");
-  static_assert(MERGE <= LDS && LDS <= kLdsLimit, "LDS budget");
+  static constexpr int TILE = KT * ROWB;
+  static constexpr int RPL = 1024 / ROWB;                  // rows a wave's load covers
+  static constexpr int LOADS = KT / RPL;                   // loads of a tile
+  static constexpr int SWZ = 16 / RPL;                     // loads after which the swizzles repeat
+  static constexpr int LDS = WAVES * 2 * TILE;
+  static constexpr int MERGE = (WAVES - 1) * 32 * (DP + 4) * 4;   // join of the waves' parts
+  static_assert(MERGE <= LDS && 2 * LDS <= kLdsLimit, "two workgroups a compute unit");
 };
 
 // Position of chunk c of row r.
@@ -175,21 +172,26 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const f32x16 (&o)
         l == 0.f ? -INFINITY : (m + __builtin_log2f(l)) * 0.6931471805599453f;
 }
 
+// ------------------------------------------------------------------ few rows
+//
+// Bound by reading K and V. The waves of a workgroup take 32-key tiles of its
+// share in turn, each through LDS of its own and without meeting the others: K
+// of the next tile is asked for as soon as this one's scores have been read
+// from it, V after the products, so that each of the 8 waves of a compute unit
+// keeps 8 to 16 KiB in flight. They join in LDS at the end.
 template <bool F16, class C>
-__global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams p) {
+__global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const AttnParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
   constexpr int DK = C::DP / 16, DT = C::DP / 32;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wq = wave % C::WQ, wk = wave / C::WQ;
   const int l32 = lane & 31, h = lane >> 5;
-
-  const Share w = share_of<C::KT>(p);
+  const Share w = share_of<C::KT * C::WAVES>(p);
   const int b = w.b, kvh = w.kvh, len = w.len, D = p.D;
   const int nt = (len + C::KT - 1) / C::KT;
 
   // this lane's query row
-  const int row = w.tile * C::ROWS + wq * 32 + l32;
+  const int row = w.tile * C::ROWS + l32;
   const int rowc = min(row, p.rows - 1);
   const int tok = rowc / p.group, hq = kvh * p.group + rowc % p.group;
   u32x4 qv[DK];
@@ -202,30 +204,34 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams 
     }
   }
 
-  // stage loads: round u covers rows u RPR .. of the stage; lane -> (row,
-  // chunk position); chunks past D are out of every range
-  const int dr = tid / C::CH, dp = tid % C::CH;
-  const int kc = k_chunk<C>(dr, dp), vc = v_chunk<C>(dr, dp);
-  static_assert(C::RPR % 16 == 0, "the swizzles repeat every 16 rows");
+  // load u of a tile covers rows u RPL ..; lane -> (row, chunk position);
+  // chunks past D are out of every range and read zeros
+  const int dr = lane / C::CH, dp = lane % C::CH;
   const uint32_t kst = uint32_t(p.ks[1]) * 2u, vst = uint32_t(p.vs[1]) * 2u;   // token strides in bytes
-  const bool klive = kc * 8 < D, vlive = vc * 8 < D;
-  const uint32_t koff = klive ? uint32_t(dr) * kst + uint32_t(kc) * 16u : 0xFFFFFFF0u, kstep = klive ? C::RPR * kst : 0u;
-  const uint32_t voff = vlive ? uint32_t(dr) * vst + uint32_t(vc) * 16u : 0xFFFFFFF0u, vstep = vlive ? C::RPR * vst : 0u;
+  uint32_t koff[C::SWZ], voff[C::SWZ];
+#pragma unroll
+  for (int u = 0; u < C::SWZ; ++u) {
+    const int r = u * C::RPL + dr, kc = k_chunk<C>(r, dp), vc = v_chunk<C>(r, dp);
+    koff[u] = kc * 8 < D ? uint32_t(r) * kst + uint32_t(kc) * 16u : 0xFFFFFFF0u;
+    voff[u] = vc * 8 < D ? uint32_t(r) * vst + uint32_t(vc) * 16u : 0xFFFFFFF0u;
+  }
   const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k + int64_t(b) * p.ks[0] + int64_t(kvh) * p.ks[2] + int64_t(w.first) * p.ks[1]);
   const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v + int64_t(b) * p.vs[0] + int64_t(kvh) * p.vs[2] + int64_t(w.first) * p.vs[1]);
-  const uint32_t lds0 = lds_address(smem) + wave * 1024;
-  auto load_stage = [&](int t) __attribute__((always_inline)) {
-    const uint32_t dst = lds0 + (t & 1) * 2 * C::TILE;
-    // (rows - 1) strides and one row: below 2^31, strides are below 2^24 bytes
-    const int rows = min(len - t * C::KT, C::KT);
-    const u32x4 kr = range_desc(kb + int64_t(t * C::KT) * kst, uint32_t(rows - 1) * kst + uint32_t(D) * 2u);
-    const u32x4 vr = range_desc(vb + int64_t(t * C::KT) * vst, uint32_t(rows - 1) * vst + uint32_t(D) * 2u);
+  const uint8_t* kt = smem + wave * 2 * C::TILE;
+  const uint8_t* vt = kt + C::TILE;
+  // the 16 rows from `half` on of tile t (an empty range past the last key: the
+  // same loads, which read nothing, so that every wait counts alike)
+  auto load = [&](const uint8_t* base, uint32_t stride, const uint32_t (&off)[C::SWZ], int t, uint32_t to) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < C::ROUNDS; ++u) {
-      load_to_lds(kr, koff + u * kstep, dst + u * C::RPR * C::ROWB);
-      load_to_lds(vr, voff + u * vstep, dst + u * C::RPR * C::ROWB + C::TILE);
+    for (int half = 0; half < 2; ++half) {
+      const int r0 = t * C::KT + 16 * half, rows = min(len - r0, 16);
+      const uint32_t any = uint32_t(-rows >> 31);   // all ones where rows > 0
+      const u32x4 rs = range_desc(base + int64_t(r0) * stride, (uint32_t(rows - 1) * stride + uint32_t(D) * 2u) & any);
+#pragma unroll
+      for (int u = 0; u < C::SWZ; ++u) load_to_lds(rs, off[u], to + (half * C::SWZ + u) * 1024);
     }
   };
+  const uint32_t kto = lds_address(kt), vto = lds_address(vt);
 
   f32x16 o[DT];
 #pragma unroll
@@ -234,85 +240,77 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams 
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   float m = -INFINITY, l = 0.f;   // maximum in log2 units; this lane's part of the sum
 
-  // addresses of this lane's reads inside a stage
-  const int krow = wk * 32 * C::NKT + l32;
-  const int vr = (lane & 15) >> 2;                       // row of the four
-  const int vcol = 4 * ((lane >> 4) & 1) + (lane & 3);   // run of 4 values among the 32 of a d tile
-
-  if (nt > 0) load_stage(0);
-  for (int t = 0; t < nt; ++t) {
-    wait_vm_lgkm0<0>();
-    __syncthreads();
-    if (t + 1 < nt) load_stage(t + 1);
-    const uint8_t* st = smem + (t & 1) * 2 * C::TILE;
-
-    f32x16 sc[C::NKT];
+  if (wave < nt) {
+    load(kb, kst, koff, wave, kto);
+    load(vb, vst, voff, wave, vto);
+  }
+  for (int t = wave; t < nt; t += C::WAVES) {
+    wait_vm<C::LOADS>();   // K of tile t; V's loads are younger
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    f32x16 sc;
 #pragma unroll
-    for (int j = 0; j < C::NKT; ++j) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sc[j][i] = 0.f;
-#pragma unroll
-      for (int s = 0; s < DK; ++s) {
-        const int r = krow + 32 * j;
-        const u32x4 a = *reinterpret_cast<const u32x4*>(st + r * C::ROWB + k_chunk<C>(r, 2 * s + h) * 16);
-        sc[j] = mfma32<F16>(a, qv[s], sc[j]);
-      }
+    for (int s = 0; s < DK; ++s) {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(kt + l32 * C::ROWB + k_chunk<C>(l32, 2 * s + h) * 16);
+      sc = mfma32<F16>(a, qv[s], s == 0 ? f32x16{} : sc);
     }
-    if ((t + 1) * C::KT > len) {   // the sequence ends in this stage
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm_lgkm0<63>();   // K is read
+    load(kb, kst, koff, t + C::WAVES, kto);
+    if ((t + 1) * C::KT > len) {   // the keys end in this tile
 #pragma unroll
-      for (int j = 0; j < C::NKT; ++j)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = t * C::KT + wk * 32 * C::NKT + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3);
-          if (key >= len) sc[j][i] = -INFINITY;
-        }
+      for (int i = 0; i < 16; ++i)
+        if (t * C::KT + 8 * (i >> 2) + 4 * h + (i & 3) >= len) sc[i] = -INFINITY;
     }
-    float top = sc[0][0];
+    float top = sc[0];
 #pragma unroll
-    for (int j = 0; j < C::NKT; ++j)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[j][i]);
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, sc[i]);
     top = other_max(top) * p.c;
     const float mn = fmaxf(m, top);
     const float ms = mn == -INFINITY ? 0.f : mn;   // no key yet, or none with weight
-    const float alpha = __builtin_amdgcn_exp2f(m - ms);
+    if (__builtin_amdgcn_ballot_w64(mn != m)) {
+      const float alpha = __builtin_amdgcn_exp2f(m - ms);
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+    }
     m = mn;
-    l *= alpha;
+    u32x4 pv[2];
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+    for (int i = 0; i < 16; i += 2) {
+      const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], p.c, -ms));
+      const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i + 1], p.c, -ms));
+      l += e0 + e1;
+      pv[i >> 3][(i >> 1) & 3] = narrow2<F16>(e0, e1);
+    }
+    wait_vm<C::LOADS>();   // V of tile t; the next K's loads are younger
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
-    u32x4 pv[2 * C::NKT];
-#pragma unroll
-    for (int j = 0; j < C::NKT; ++j)
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][i], p.c, -ms));
-        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][i + 1], p.c, -ms));
-        l += e0 + e1;
-        pv[2 * j + (i >> 3)][(i >> 1) & 3] = narrow2<F16>(e0, e1);
-      }
-#pragma unroll
-    for (int j = 0; j < 2 * C::NKT; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        const int r0 = wk * 32 * C::NKT + 16 * j + 4 * h + vr;
-        const int col = 8 * d + vcol;   // run of 4 values in the row
-        const u32x2 lo = read_transposed(st + C::TILE + r0 * C::ROWB + v_chunk<C>(r0, col >> 1) * 16 + (col & 1) * 8);
-        const u32x2 hi = read_transposed(st + C::TILE + (r0 + 8) * C::ROWB + v_chunk<C>(r0 + 8, col >> 1) * 16 + (col & 1) * 8);
+        const int r = 16 * j + 4 * h + ((lane & 15) >> 2), run = 8 * d + 4 * ((lane >> 4) & 1) + (lane & 3);
+        const uint8_t* v = vt + r * C::ROWB + v_chunk<C>(r, run >> 1) * 16 + (run & 1) * 8;
+        const u32x2 lo = read_transposed(v), hi = read_transposed(v + 8 * C::ROWB);
         o[d] = mfma32<F16>(u32x4{lo.x, lo.y, hi.x, hi.y}, pv[j], o[d]);
       }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm_lgkm0<63>();   // V is read
+    load(vb, vst, voff, t + C::WAVES, vto);
   }
+  wait_vm<0>();
   l = other_sum(l);
 
-  if constexpr (C::WK > 1) {
-    // join the waves' keys: each writes its sums, maximum and sum; wave 0 adds
-    // them in order
-    static_assert(C::WQ == 1, "waves over keys share one row tile");
-    float* mg = reinterpret_cast<float*>(smem);
-    constexpr int S = C::DP + 4;
-    __syncthreads();
-    float* mine = mg + (wk * 32 + l32) * S;
+  // join the waves' keys: the others write their sums, maximum and sum; wave 0
+  // adds them in order
+  float* mg = reinterpret_cast<float*>(smem);
+  constexpr int S = C::DP + 4;
+  __syncthreads();
+  if (wave != 0) {
+    float* mine = mg + ((wave - 1) * 32 + l32) * S;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -322,37 +320,35 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(const AttnParams 
       mine[C::DP] = m;
       mine[C::DP + 1] = l;
     }
-    __syncthreads();
-    if (wk != 0) return;
-    float mm = m;
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  float mm = m;
 #pragma unroll
-    for (int v = 1; v < C::WK; ++v) mm = fmaxf(mm, mg[(v * 32 + l32) * S + C::DP]);
-    const float ms = mm == -INFINITY ? 0.f : mm;
-    const float f0 = __builtin_amdgcn_exp2f(m - ms);
-    l *= f0;
+  for (int v = 0; v < C::WAVES - 1; ++v) mm = fmaxf(mm, mg[(v * 32 + l32) * S + C::DP]);
+  const float ms = mm == -INFINITY ? 0.f : mm;
+  const float f0 = __builtin_amdgcn_exp2f(m - ms);
+  l *= f0;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] *= f0;
+#pragma unroll
+  for (int v = 0; v < C::WAVES - 1; ++v) {
+    const float* other = mg + (v * 32 + l32) * S;
+    const float f = __builtin_amdgcn_exp2f(other[C::DP] - ms);
+    l += other[C::DP + 1] * f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[d][i] *= f0;
+      for (int i = 0; i < 16; i += 4) {
+        const f32x4 w4 = *reinterpret_cast<const f32x4*>(other + 32 * d + 2 * i + 4 * h);
 #pragma unroll
-    for (int v = 1; v < C::WK; ++v) {
-      const float* other = mg + (v * 32 + l32) * S;
-      const float f = __builtin_amdgcn_exp2f(other[C::DP] - ms);
-      l += other[C::DP + 1] * f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const f32x4 w4 = *reinterpret_cast<const f32x4*>(other + 32 * d + 2 * i + 4 * h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[d][i + e] += w4[e] * f;
-        }
-    }
-    m = mm;
+        for (int e = 0; e < 4; ++e) o[d][i + e] += w4[e] * f;
+      }
   }
-
   if (row >= p.rows) return;
-  store_row<F16, C>(p, o, m, l, w, wq * 32 + l32, tok, hq, h);
+  store_row<F16, C>(p, o, mm, l, w, l32, tok, hq, h);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -613,7 +609,6 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
 }
 
 // Joins the parts of the cut tiles' rows, in order: one thread per 4 values.
-// The loads of several parts are in flight at once.
 template <bool F16>
 __global__ __launch_bounds__(256) void attention_join_kernel(const AttnParams p, int tile_rows) {
   const int per = p.D / 4;
@@ -627,17 +622,34 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnParams p,
   const int64_t at = int64_t(nth) * p.parts * tile_rows + r;
   const float* ms = p.part_ms + at * 2;
   const float* po = p.part_o + at * p.D + e;
-  float mm = -INFINITY;
-#pragma unroll 8
-  for (int s = 0; s < p.parts; ++s) mm = fmaxf(mm, ms[int64_t(s) * tile_rows * 2]);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float l = 0.f;
+  // eight parts at a time, their loads in flight together
+  float mm = -INFINITY, l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int s = 0; s < p.parts; ++s) {
-    const float f = __builtin_amdgcn_exp2f(ms[int64_t(s) * tile_rows * 2] - base);
-    l += ms[int64_t(s) * tile_rows * 2 + 1] * f;
-    o += *reinterpret_cast<const f32x4*>(po + int64_t(s) * tile_rows * p.D) * f;
+  for (int s0 = 0; s0 < p.parts; s0 += 8) {
+    float pm[8], pl[8];
+    f32x4 po8[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t s = min(s0 + k, p.parts - 1);
+      pm[k] = s0 + k < p.parts ? ms[s * tile_rows * 2] : -INFINITY;
+      pl[k] = ms[s * tile_rows * 2 + 1];
+      po8[k] = *reinterpret_cast<const f32x4*>(po + s * tile_rows * p.D);
+    }
+    float mn = mm;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mn = fmaxf(mn, pm[k]);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float f0 = __builtin_amdgcn_exp2f(mm - base);
+    l *= f0;
+    o *= f0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k < p.parts) {
+        const float f = __builtin_amdgcn_exp2f(pm[k] - base);
+        l += pl[k] * f;
+        o += po8[k] * f;
+      }
+    mm = mn;
   }
   const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
   const int b = pair / p.kv_heads, tok = row / p.group, hq = (pair - b * p.kv_heads) * p.group + row % p.group;
@@ -667,8 +679,8 @@ static bool attn_sizes_ok(const cross_attention_t* a) {
 }
 
 // Tiles and which of them are cut. Up to 32 rows (token, query head of the
-// group) a pair: the few-row kernel, one workgroup a compute unit; else 128-row
-// tiles, two a compute unit. Tiles that fill no whole round of the compute
+// group) a pair: the few-row kernel; else 128-row tiles; two workgroups a
+// compute unit. Tiles that fill no whole round of the compute
 // units are cut into the parts that would fill it, of at least kMinPart keys.
 static AttnPlan attn_plan(const cross_attention_t* a) {
   constexpr int kMinPart = 256;
@@ -700,9 +712,9 @@ static AttnPlan attn_plan(const cross_attention_t* a) {
 template <bool F16>
 static const void* attention_of(bool few, int D) {
   if (few)
-    return D <= 64 ? reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<64, 1, 4, 128>>)
-         : D <= 96 ? reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<96, 1, 4, 128>>)
-                   : reinterpret_cast<const void*>(attention_kernel<F16, AttnCfg<128, 1, 4, 128>>);
+    return D <= 64 ? reinterpret_cast<const void*>(attention_few_kernel<F16, FewAttn<64>>)
+         : D <= 96 ? reinterpret_cast<const void*>(attention_few_kernel<F16, FewAttn<96>>)
+                   : reinterpret_cast<const void*>(attention_few_kernel<F16, FewAttn<128>>);
   return D <= 64 ? reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<64>>)
        : D <= 96 ? reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<96>>)
                  : reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<128>>);
