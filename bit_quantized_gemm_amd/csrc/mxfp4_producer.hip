@@ -2,11 +2,13 @@
 // gemm_mxfp4 (E2M1 codes [M, K/2], one UE8M0 scale per 32 k at [K/32, M]) and
 // lora_act_in [M, R] = x @ lora_down^T (quantize_mxfp4_act in gemm_w4a4.h).
 //
-// Bound by memory: 2 bytes read and 17/32 written an element. x is read once:
-// lane (r, g) of a wave holds row r, k = 32 g .. 32 g + 31 of a 128-wide span,
-// one whole scale block, so its largest magnitude needs no other lane, and the
-// same registers are the A operand of the LoRA product (the order of k is free
-// as long as lora_down is read in the same one).
+// Bound by memory: 2 bytes read and 17/32 written an element. x is read once,
+// in the layout of the LoRA product's A operand: lane (r, g) of a wave holds row
+// r, k = 32 i + 8 g .. + 7 for the four blocks i of a 128-wide span, so that
+// four lanes read 64 neighbouring bytes (one whole block a lane, 64 bytes
+// apart, cost four times the cache cycles: 14.2 us at 4096 x 3072, R = 32).
+// A block's largest magnitude meets over its four lanes by lane swaps, and so
+// do its codes, which leave as 16 bytes a lane.
 //
 // The scale of a block is a power of two read off the exponent of its largest
 // magnitude, and gfx950's FP4 conversion divides by a power of two and rounds
@@ -26,6 +28,7 @@
 #include <algorithm>
 
 #include "gemm_w4a4.h"
+#include "w4a4_buffer.hpp"
 #include "w4a4_common.hpp"
 #include "w4a4_half.hpp"
 #include "w4a4_host.hpp"
@@ -43,104 +46,161 @@ struct MxProdParams {
   int ks, sps;          // K slices, spans per slice
 };
 
-// 32 values (16 dwords, low half = even k) of one block -> its scale byte and
-// codes. Magnitudes order like their bit patterns, NaN above infinity above
-// every finite value: a packed 16-bit max.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// max over the lanes l, l ^ 16, l ^ 32, l ^ 48, of both halves of a dword
+__device__ __forceinline__ u16x2 max_of_four(u16x2 v) {
+  const uint32_t a = __builtin_bit_cast(uint32_t, v);
+  const auto s = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+  const u16x2 m = __builtin_elementwise_max(__builtin_bit_cast(u16x2, uint32_t(s[0])), __builtin_bit_cast(u16x2, uint32_t(s[1])));
+  const uint32_t b = __builtin_bit_cast(uint32_t, m);
+  const auto t = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return __builtin_elementwise_max(__builtin_bit_cast(u16x2, uint32_t(t[0])), __builtin_bit_cast(u16x2, uint32_t(t[1])));
+}
+
+// 8 values (low half = even k) divided by a power of two -> 8 codes. (The
+// dwords are copied out first: this compiler's bit-cast of a vector element
+// reads the vector's first one.)
 template <bool F16>
-__device__ __forceinline__ uint32_t quantize_block32(const uint32_t (&d)[16], u32x4& codes) {
-  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  u16x2 m = __builtin_bit_cast(u16x2, d[0] & 0x7FFF7FFFu);
-#pragma unroll
-  for (int i = 1; i < 16; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, d[i] & 0x7FFF7FFFu));
-  const uint32_t top = max(uint32_t(m[0]), uint32_t(m[1]));
-  const bool finite = top < (F16 ? 0x7C00u : 0x7F80u);
-  // biased float32 exponent of the largest magnitude (a binary16 subnormal is
-  // a normal float32; a bfloat16 one has exponent 0, which the max covers)
-  const uint32_t e = __builtin_bit_cast(uint32_t, widen<F16>(uint16_t(finite ? top : 0u))) >> 23;
-  const uint32_t byte = uint32_t(max(int(e) - 2, 0));
-  const float scale = __builtin_bit_cast(float, byte == 0 ? 0x00400000u : byte << 23);   // 2^(byte - 127)
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if constexpr (F16) {
-      const f16x2 v = __builtin_bit_cast(f16x2, d[i]);
-      switch (i & 3) {   // the byte must be an immediate; folds after unrolling
-        case 0: w[i >> 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w[i >> 2], v, scale, 0); break;
-        case 1: w[i >> 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w[i >> 2], v, scale, 1); break;
-        case 2: w[i >> 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w[i >> 2], v, scale, 2); break;
-        default: w[i >> 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w[i >> 2], v, scale, 3); break;
-      }
-    } else {
-      const bf16x2 v = __builtin_bit_cast(bf16x2, d[i]);
-      switch (i & 3) {
-        case 0: w[i >> 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i >> 2], v, scale, 0); break;
-        case 1: w[i >> 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i >> 2], v, scale, 1); break;
-        case 2: w[i >> 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i >> 2], v, scale, 2); break;
-        default: w[i >> 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i >> 2], v, scale, 3); break;
-      }
-    }
+__device__ __forceinline__ uint32_t codes_of(const u32x4& d, float scale) {
+  uint32_t w = 0u;
+  const uint32_t d0 = d.x, d1 = d.y, d2 = d.z, d3 = d.w;
+  if constexpr (F16) {
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, __builtin_bit_cast(f16x2, d0), scale, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, __builtin_bit_cast(f16x2, d1), scale, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, __builtin_bit_cast(f16x2, d2), scale, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, __builtin_bit_cast(f16x2, d3), scale, 3);
+  } else {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, d0), scale, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, d1), scale, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, d2), scale, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, d3), scale, 3);
   }
-  codes = finite ? u32x4{w[0], w[1], w[2], w[3]} : u32x4{0u, 0u, 0u, 0u};
-  return finite ? byte : 0xFFu;
+  return w;
+}
+
+// The four blocks of a span, d[i] this lane's 8 values of block i -> the
+// scale byte and the 16 bytes of codes of block g. Magnitudes order like their
+// bit patterns, NaN above infinity above every finite value.
+template <bool F16>
+__device__ __forceinline__ uint32_t quantize_span(const u32x4 (&d)[4], int g, u32x4& codes) {
+  u16x2 pairs[2];   // maxima of blocks 0 and 1, 2 and 3
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    u16x2 m = __builtin_bit_cast(u16x2, d[i].x & 0x7FFF7FFFu);
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, d[i].y & 0x7FFF7FFFu));
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, d[i].z & 0x7FFF7FFFu));
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, d[i].w & 0x7FFF7FFFu));
+    pairs[i >> 1][i & 1] = m[0] > m[1] ? m[0] : m[1];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) pairs[i] = max_of_four(pairs[i]);
+  uint32_t c[4], byte[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t top = pairs[i >> 1][i & 1];
+    const bool finite = top < (F16 ? 0x7C00u : 0x7F80u);
+    // biased float32 exponent of the largest magnitude (a binary16 subnormal
+    // is a normal float32; a bfloat16 one has exponent 0, which the max covers)
+    const uint32_t e = __builtin_bit_cast(uint32_t, widen<F16>(uint16_t(finite ? top : 0u))) >> 23;
+    const uint32_t b = uint32_t(max(int(e) - 2, 0));
+    const float scale = __builtin_bit_cast(float, b == 0 ? 0x00400000u : b << 23);   // 2^(b - 127)
+    const uint32_t w = codes_of<F16>(d[i], scale);
+    c[i] = finite ? w : 0u;
+    byte[i] = finite ? b : 0xFFu;
+  }
+  // lane g's c[i] is bytes 4 g .. + 3 of block i; afterwards word s of lane g is
+  // lane s's of block g
+  const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
+  const auto lo = __builtin_amdgcn_permlane16_swap(uint32_t(a[0]), uint32_t(b[0]), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(uint32_t(a[1]), uint32_t(b[1]), false, false);
+  codes = u32x4{uint32_t(lo[0]), uint32_t(lo[1]), uint32_t(hi[0]), uint32_t(hi[1])};
+  const uint32_t b01 = g & 1 ? byte[1] : byte[0], b23 = g & 1 ? byte[3] : byte[2];
+  return g & 2 ? b23 : b01;
 }
 
 constexpr int kMxProdWaves = 8;
-constexpr int kMxProdRows = 16;
 
-// RT: rank tiles of 16 (0: no LoRA product).
+// One workgroup a 16 rows. RT: rank tiles of 16 (0: no LoRA product).
 template <bool F16, int RT>
 __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const MxProdParams p) {
-  constexpr int W = kMxProdWaves;
+  constexpr int W = kMxProdWaves, NA = RT > 0 ? RT : 1;
   __shared__ f32x4 red[RT > 0 ? W * RT * kWave : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int M = p.M, K = p.K, R = p.R;
   const int rb = blockIdx.x / p.ks, z = blockIdx.x - rb * p.ks;
-  const int m0 = rb * kMxProdRows;
+  const int m0 = rb * 16;
   const int nsp = (K + 127) / 128;
   const int s_end = min(nsp, (z + 1) * p.sps);
-  const int row = min(m0 + r, M - 1);     // rows past M repeat the last and are not stored
-  const bool live_row = m0 + r < M;
-  const uint16_t* xr = p.x + size_t(row) * size_t(K);
-  f32x4 acc[RT > 0 ? RT : 1];
+  const int row = min(m0 + r, M - 1);   // rows past M repeat the last and are not stored
+  const bool live = m0 + r < M;
+  const uint16_t* xr = p.x + size_t(row) * size_t(K) + 8 * g;
+  const uint16_t* lr[NA];
+#pragma unroll
+  for (int j = 0; j < RT; ++j)   // ranks past R repeat the last; their sums are not stored
+    lr[j] = p.lora_down + size_t(min(16 * j + r, R - 1)) * size_t(K) + 8 * g;
+  f32x4 acc[NA];
 #pragma unroll
   for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  for (int s = z * p.sps + wave; s < s_end; s += W) {
-    const int k0 = s * 128 + 32 * g;
-    const bool live = k0 < K;              // K % 32 == 0: a block is in or out whole
-    uint32_t d[16];
-    u32x4 b[RT > 0 ? RT : 1][4];
+  // A span's x, and its lora_down operands where they are few, are asked for
+  // one span ahead; many operands in halves, the first before the codes are
+  // worked out. TAIL: the span that K ends in; its blocks past K (K % 32 == 0: in
+  // or out whole) read as zeros.
+  constexpr bool AHEAD = RT <= 2;
+  constexpr int NB = RT > 4 ? 2 : 4;   // k-steps of operands held
+  u32x4 x[2][4], b[2][NB][NA];
+  auto load = [&]<bool TAIL>(const uint16_t* from, int k) __attribute__((always_inline)) {
+    return !TAIL || k < K ? *reinterpret_cast<const u32x4*>(from + k) : u32x4{0u, 0u, 0u, 0u};
+  };
+  auto load_b = [&]<bool TAIL>(u32x4 (&bs)[NB][NA], int s, int i0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x4 v = live ? *reinterpret_cast<const u32x4*>(xr + k0 + 8 * i) : u32x4{0u, 0u, 0u, 0u};
-      d[4 * i] = v.x;
-      d[4 * i + 1] = v.y;
-      d[4 * i + 2] = v.z;
-      d[4 * i + 3] = v.w;
-    }
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      // ranks past R repeat the last; their sums are not stored
-      const uint16_t* l = p.lora_down + size_t(min(16 * j + r, R - 1)) * size_t(K) + k0;
+      for (int j = 0; j < RT; ++j) bs[i][j] = load.template operator()<TAIL>(lr[j], s * 128 + 32 * (i0 + i));
+  };
+  auto products = [&](const u32x4 (&d)[4], const u32x4 (&bs)[NB][NA], int i0) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        b[j][i] = live ? *reinterpret_cast<const u32x4*>(l + 8 * i) : u32x4{0u, 0u, 0u, 0u};
-    }
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) acc[j] = mfma16<F16>(d[i0 + i], bs[i][j], acc[j]);
+  };
+  auto ask = [&]<bool TAIL>(int q, int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[q][i] = load.template operator()<TAIL>(xr, s * 128 + 32 * i);
+    if constexpr (AHEAD) load_b.template operator()<TAIL>(b[q], s, 0);
+  };
+  auto work = [&]<bool TAIL>(int q, int s) __attribute__((always_inline)) {
+    if constexpr (!AHEAD) load_b.template operator()<TAIL>(b[q], s, 0);
+    const int k = s * 128 + 32 * g;
     u32x4 codes;
-    const uint32_t byte = quantize_block32<F16>(d, codes);
-    if (live && live_row) {
-      *reinterpret_cast<u32x4*>(p.act + size_t(row) * size_t(K / 2) + k0 / 2) = codes;
-      p.ascales[size_t(k0 / 32) * size_t(M) + row] = uint8_t(byte);
+    const uint32_t byte = quantize_span<F16>(x[q], g, codes);
+    if (live && (!TAIL || k < K)) {
+      *reinterpret_cast<u32x4*>(p.act + size_t(row) * size_t(K / 2) + k / 2) = codes;
+      p.ascales[size_t(k / 32) * size_t(M) + row] = uint8_t(byte);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x4 a = {d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]};
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[j] = mfma16<F16>(a, b[j][i], acc[j]);
+    products(x[q], b[q], 0);
+    if constexpr (NB == 2) {
+      load_b.template operator()<TAIL>(b[q], s, 2);
+      products(x[q], b[q], 2);
     }
+  };
+  const int e = min(s_end, K / 128);   // past the whole spans
+  int s = z * p.sps + wave;
+  if (s < e) ask.template operator()<false>(0, s);
+  for (; s < e; s += 2 * W) {
+    if (s + W < e) ask.template operator()<false>(1, s + W);
+    work.template operator()<false>(0, s);
+    if (s + 2 * W < e) ask.template operator()<false>(0, s + 2 * W);
+    if (s + W < e) work.template operator()<false>(1, s + W);
+  }
+  if (e < s_end && (e - z * p.sps) % W == wave) {   // the span that K ends in
+    ask.template operator()<true>(0, e);
+    work.template operator()<true>(0, e);
   }
 
   if constexpr (RT > 0) {
@@ -149,20 +209,145 @@ __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const
     __syncthreads();
     // lane (c, g) of rank tile j holds rows 4g .. 4g+3 of rank 16 j + c
     for (int j = wave; j < RT; j += W) {
-      f32x4 t = red[j * kWave + lane];
+      f32x4 sum = red[j * kWave + lane];
 #pragma unroll
-      for (int w = 1; w < W; ++w) t += red[(w * RT + j) * kWave + lane];
-      const int rank = 16 * j + (lane & 15);
+      for (int w = 1; w < W; ++w) sum += red[(w * RT + j) * kWave + lane];
+      const int rank = 16 * j + r;
       if (rank >= R) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int m = m0 + 4 * g + e;
+      for (int i = 0; i < 4; ++i) {
+        const int m = m0 + 4 * g + i;
         if (m >= M) continue;
         if (p.ks > 1)
-          p.part[(size_t(z) * size_t(M) + m) * size_t(R) + rank] = t[e];
+          p.part[(size_t(z) * size_t(M) + m) * size_t(R) + rank] = sum[i];
         else
-          p.lora_act_in[size_t(m) * size_t(R) + rank] = narrow<F16>(t[e]);
+          p.lora_act_in[size_t(m) * size_t(R) + rank] = narrow<F16>(sum[i]);
       }
+    }
+  }
+}
+
+// Read per 16 rows, lora_down outweighs x by R / 16 (and both come out of the
+// same cache), so for many ranks, or many rows, a workgroup takes 16 W rows, 16 a
+// wave, and its waves share each span's lora_down tile in LDS. Both it and the
+// waves' own x come by direct-to-LDS loads two spans ahead, lora_down in a ring
+// of three, x in one of two (a wave has read its x before it asks for more).
+// The chunks of a row are XOR-swizzled by row: no read meets a bank twice.
+template <int RT_, int W_>
+struct MxShared {
+  static constexpr int RT = RT_, W = W_, ROWS = 16 * W, RING = 3;
+  static constexpr int TILE = RT * 16 * 256;          // a span of lora_down
+  static constexpr int LOADS = RT * 4 / W;            // a wave's loads of it, 4 ranks each
+  static constexpr int XTILE = 16 * 256;              // a span of a wave's x, 4 loads
+  static constexpr int XOFF = RING * TILE;
+  static constexpr int LDS = XOFF + W * 2 * XTILE;
+  // loads of the span after the one that is needed (the stores of codes among
+  // them only make the wait longer)
+  static constexpr int YOUNGER = LOADS + 4;
+  static_assert(RT * 4 % W == 0 && LDS <= kLdsLimit && YOUNGER < 64, "LDS and wait counter");
+};
+
+template <bool F16, class C>
+__global__ __launch_bounds__(C::W * kWave) void mx_producer_shared_kernel(const MxProdParams p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
+  constexpr int RT = C::RT;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int M = p.M, K = p.K, R = p.R;
+  const int rb = blockIdx.x / p.ks, z = blockIdx.x - rb * p.ks;
+  const int mw = rb * C::ROWS + 16 * wave;
+  const int nsp = (K + 127) / 128;
+  const int s_beg = z * p.sps, s_end = min(nsp, s_beg + p.sps);
+  const uint32_t row_bytes = uint32_t(K) * 2u, l_bytes = uint32_t(R) * row_bytes, x_bytes = uint32_t(M) * row_bytes;
+  // this lane's place in a load: row 4 u + lane / 16 of the tile, chunk position
+  // lane % 16. Rows past M repeat the last and are not stored; ranks past R are
+  // past the tensor (zeros).
+  uint32_t loff[C::LOADS], xoff[4];
+  int xk[4], lk[C::LOADS];   // first k of the lane's chunk in the span
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    xk[u] = 8 * (r ^ (4 * u + g));
+    xoff[u] = uint32_t(min(mw + 4 * u + g, M - 1)) * row_bytes + uint32_t(xk[u]) * 2u;
+  }
+#pragma unroll
+  for (int u = 0; u < C::LOADS; ++u) {
+    const int rank = (wave * C::LOADS + u) * 4 + g;
+    lk[u] = 8 * (r ^ (rank & 15));
+    loff[u] = uint32_t(rank) * row_bytes + uint32_t(lk[u]) * 2u;
+  }
+  const uint32_t lds_l = lds_address(smem) + wave * C::LOADS * 1024;
+  const uint32_t lds_x = lds_address(smem) + C::XOFF + wave * 2 * C::XTILE;
+  // What lies past K, and whole spans past the slice, read as zeros: offsets
+  // out of every range.
+  auto ask_x = [&](int s, int place) __attribute__((always_inline)) {
+    const bool in = s < s_end;
+    const uint32_t at = in ? uint32_t(s) * 256u : 0u;
+    const u32x4 d = range_desc(reinterpret_cast<const uint8_t*>(p.x) + at, in ? x_bytes - at : 0u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_to_lds(d, s * 128 + xk[u] < K ? xoff[u] : 0xFFFFFFF0u, lds_x + place * C::XTILE + u * 1024);
+  };
+  auto ask_l = [&](int s, int place) __attribute__((always_inline)) {
+    const bool in = s < s_end;
+    const uint32_t at = in ? uint32_t(s) * 256u : 0u;
+    const u32x4 d = range_desc(reinterpret_cast<const uint8_t*>(p.lora_down) + at, in ? l_bytes - at : 0u);
+#pragma unroll
+    for (int u = 0; u < C::LOADS; ++u) load_to_lds(d, s * 128 + lk[u] < K ? loff[u] : 0xFFFFFFF0u, lds_l + place * C::TILE + u * 1024);
+  };
+  f32x4 acc[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const bool live = mw + r < M;
+  const int row = min(mw + r, M - 1);
+
+  ask_x(s_beg, 0);
+  ask_l(s_beg, 0);
+  ask_x(s_beg + 1, 1);
+  ask_l(s_beg + 1, 1);
+  int place = 0;   // of the span in the ring of three
+  for (int s = s_beg; s < s_end; ++s) {
+    wait_vm_lgkm0<C::YOUNGER>();   // this wave's loads of the span
+    wg_barrier();                  // everyone's, and everyone past the span before
+    const int xp = (s - s_beg) & 1;
+    u32x4 x[4], codes;
+    const uint8_t* xt = smem + C::XOFF + (wave * 2 + xp) * C::XTILE + r * 256;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const u32x4*>(xt + (((4 * i + g) ^ r) << 4));
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm_lgkm0<63>();           // x is read
+    ask_x(s + 2, xp);
+    ask_l(s + 2, place == 0 ? 2 : place - 1);
+    const uint32_t byte = quantize_span<F16>(x, g, codes);
+    const int k = s * 128 + 32 * g;
+    if (live && k < K) {
+      *reinterpret_cast<u32x4*>(p.act + size_t(row) * size_t(K / 2) + k / 2) = codes;
+      p.ascales[size_t(k / 32) * size_t(M) + row] = uint8_t(byte);
+    }
+    const uint8_t* t = smem + place * C::TILE + r * 256;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const u32x4 b = *reinterpret_cast<const u32x4*>(t + j * 4096 + (((4 * i + g) ^ r) << 4));
+        acc[j] = mfma16<F16>(x[i], b, acc[j]);
+      }
+    place = place == 2 ? 0 : place + 1;
+  }
+  wait_vm<0>();
+
+  // lane (c, g) of tile j holds rows 4g .. 4g+3 of rank 16 j + c
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    const int rank = 16 * j + r;
+    if (rank >= R) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int m = mw + 4 * g + e;
+      if (m >= M) continue;
+      if (p.ks > 1)
+        p.part[(size_t(z) * size_t(M) + m) * size_t(R) + rank] = acc[j][e];
+      else
+        p.lora_act_in[size_t(m) * size_t(R) + rank] = narrow<F16>(acc[j][e]);
     }
   }
 }
@@ -193,14 +378,30 @@ static int mx_cus() {
 }
 
 struct MxProdPlan {
-  int ks, sps;
+  int shared;    // waves of the kernel that shares lora_down; 0: the other
+  int threads;
+  int rbs;       // row blocks
+  int ks, sps;   // K slices, spans of a slice
   int64_t bytes;
 };
 
+// Which kernel, measured (binary16, us, unshared against shared of 4 waves):
+// 4096x3072 R=32 11.9 against 15.2, 4096x12288 R=32 41.6 against 29.8,
+// 16384x3072 R=32 43.2 against 26.8, 1001x12288 R=128 24.8 against 18.9: shared
+// for more than 32 ranks, and for fewer where x is large. 8 waves of shared
+// against 4: 1001x12288 R=128 19.9 and 18.9, 4096x12288 R=128 41.0 and 46.7,
+// R=64 33.5 and 31.9: for more than 64 ranks of many rows.
 static MxProdPlan mx_prod_plan(int M, int K, int R) {
-  const int rbs = (M + kMxProdRows - 1) / kMxProdRows, nsp = (K + 127) / 128;
-  const int ks = std::max(1, std::min((nsp + kMxProdWaves - 1) / kMxProdWaves, mx_cus() / rbs));
   MxProdPlan pl;
+  const bool large = M > 4096 || int64_t(M) * K >= (int64_t(1) << 25);
+  pl.shared = R > 32 ? (M <= 16 ? 0 : R > 64 && M >= 2048 ? 8 : 4) : R > 0 && large ? 4 : 0;
+  const int waves = pl.shared ? pl.shared : kMxProdWaves, rows = pl.shared ? 16 * waves : 16;
+  pl.threads = waves * kWave;
+  pl.rbs = (M + rows - 1) / rows;
+  const int nsp = (K + 127) / 128;
+  // slices that fill the chip once; of at least 2 spans a wave, or 3 of a
+  // workgroup that shares them
+  const int ks = std::max(1, std::min(nsp / (pl.shared ? 3 : 2 * waves), mx_cus() / pl.rbs));
   pl.sps = (nsp + ks - 1) / ks;
   pl.ks = (nsp + pl.sps - 1) / pl.sps;
   pl.bytes = pl.ks > 1 && R > 0 ? int64_t(pl.ks) * M * R * 4 : 0;
@@ -214,7 +415,12 @@ static bool mx_prod_sizes_ok(int M, int K, int R) {
 }
 
 template <bool F16>
-static const void* mx_producer_of(int R) {
+static const void* mx_producer_of(int R, int shared) {
+  if (shared == 8) return reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<8, 8>>);
+  if (shared)
+    return R <= 32 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<2, 4>>)
+         : R <= 64 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<4, 4>>)
+                   : reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<8, 4>>);
   if (R == 0) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 0>);
   if (R <= 16) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 1>);
   if (R <= 32) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 2>);
@@ -251,9 +457,8 @@ static int mx_quantize_run(const uint16_t* x, const uint16_t* lora_down, uint8_t
   MxProdParams p{x, lora_down, act, ascales, lora_act_in, static_cast<float*>(workspace), M, K, R, pl.ks, pl.sps};
   void* args[] = {&p};
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const int rbs = (M + kMxProdRows - 1) / kMxProdRows;
-  hipError_t e = hipLaunchKernel(mx_producer_of<F16>(R), dim3(unsigned(rbs) * unsigned(pl.ks)),
-                                 dim3(kMxProdWaves * kWave), args, 0, st);
+  hipError_t e = hipLaunchKernel(mx_producer_of<F16>(R, pl.shared), dim3(unsigned(pl.rbs) * unsigned(pl.ks)),
+                                 dim3(pl.threads), args, 0, st);
   if (e == hipSuccess && pl.bytes > 0)
     e = hipLaunchKernel(reinterpret_cast<const void*>(mx_producer_join_kernel<F16>),
                         dim3(unsigned((Ms * Rs + 255) / 256)), dim3(256), args, 0, st);
