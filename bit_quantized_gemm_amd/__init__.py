@@ -214,8 +214,8 @@ def _half(t, name):
 
 
 def _dense(t, name, dtype, shape, device):
-    """_check in the order that passes fastest."""
-    if not (t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.device == device):
+    """_check in the order that passes fastest (get_device: the GPU's index, -1 off one)."""
+    if not (t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.get_device() == device.index):
         _check(t, name, dtype, shape, device)
 
 

@@ -5,8 +5,8 @@
 //
 // Bound by the weight bytes, N (K/2 + K/32): every weight is read once, from
 // HBM straight into the registers that the matrix instruction takes, since no
-// two waves share one. A workgroup owns 16 columns; its waves split K in steps
-// of 128 and add their sums through LDS. v_mfma_scale_f32_16x16x128_f8f6f4
+// two waves share one. A workgroup owns 16 or 32 columns; its waves split K in
+// steps of 128 and add their sums through LDS. v_mfma_scale_f32_16x16x128_f8f6f4
 // with FP4 operands: lane (c, g) holds row c, k = 32 g .. 32 g + 31 as 16 bytes
 // and that block's scale byte. The weights are its A operand (rows n) and the
 // activations, which stay in cache, its B operand (columns m), so that a lane
@@ -34,25 +34,34 @@ __device__ __forceinline__ f32x4 mfma_fp4_16(u32x4 a, u32x4 b, f32x4 c, uint32_t
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, int(sa), 0, int(sb));
 }
 
-constexpr int kFewWaves = 8;
-constexpr int kFewCols = 16;
+// MT tiles of 16 rows (M <= 16 MT), NT of 16 columns, W waves, P steps a run (of
+// a row's neighbouring bytes).
+template <int MT_, int NT_, int W_, int P_>
+struct FewCfg {
+  static constexpr int MT = MT_, NT = NT_, W = W_, P = P_, THREADS = W * kWave, COLS = 16 * NT;
+};
 
-// MT: tiles of 16 rows (M <= 16 MT).
-template <bool F16, int MT>
-__global__ __launch_bounds__(kFewWaves * kWave) void mx_few_kernel(const Params p) {
-  constexpr int W = kFewWaves;
-  __shared__ f32x4 red[W * MT * kWave];
+template <bool F16, class C>
+__global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p) {
+  constexpr int W = C::W, MT = C::MT, NT = C::NT, P = C::P;
+  __shared__ f32x4 red[W * NT * MT * kWave];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int M = p.M, N = p.N, K = p.K, R = p.R;
-  const int n0 = blockIdx.x * kFewCols;
+  const int n0 = blockIdx.x * C::COLS;
   const int kb_all = K >> 5;
   const uint32_t rowbytes = uint32_t(K) >> 1;
   // rows and columns past the edge repeat the last and are not stored
-  const int n = min(n0 + c, N - 1);
-  const uint8_t* w = p.wgt + uint32_t(n) * rowbytes + 16 * g;
-  const uint8_t* ws = p.wscales + n;
+  int n[NT];
+  const uint8_t* w[NT];
+  const uint8_t* ws[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    n[j] = min(n0 + 16 * j + c, N - 1);
+    w[j] = p.wgt + uint32_t(n[j]) * rowbytes + 16 * g;
+    ws[j] = p.wscales + n[j];
+  }
   const uint8_t* a[MT];
   const uint8_t* as[MT];
 #pragma unroll
@@ -61,40 +70,66 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_few_kernel(const Params 
     a[t] = p.act + uint32_t(m) * rowbytes + 16 * g;
     as[t] = p.ascales + m;
   }
-  f32x4 acc[MT];
+  f32x4 acc[NT][MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int steps = (K + 127) >> 7;
-  for (int s = wave; s < steps; s += W) {
-    const int kb = 4 * s + g;
-    const bool live = kb < kb_all;      // K % 128 != 0: blocks past K are zeros of scale one
-    const u32x4 wv = live ? *reinterpret_cast<const u32x4*>(w + 64 * s) : u32x4{0u, 0u, 0u, 0u};
-    const uint32_t wsc = live ? ws[uint32_t(kb) * uint32_t(N)] : 127u;
+  // TAIL: the run that K ends in
+  auto run = [&]<bool TAIL>(int s0) __attribute__((always_inline)) {
+    u32x4 wv[P][NT], av[P][MT];
+    uint32_t wsv[P][NT], asv[P][MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const u32x4 av = live ? *reinterpret_cast<const u32x4*>(a[t] + 64 * s) : u32x4{0u, 0u, 0u, 0u};
-      const uint32_t asc = live ? as[t][uint32_t(kb) * uint32_t(M)] : 127u;
-      acc[t] = mfma_fp4_16(wv, av, acc[t], wsc, asc);
+    for (int i = 0; i < P; ++i) {
+      const int s = s0 + i, kb = 4 * s + g;
+      const bool in = !TAIL || kb < kb_all;   // blocks past K are zeros of scale one
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        wv[i][j] = in ? *reinterpret_cast<const u32x4*>(w[j] + 64 * s) : u32x4{0u, 0u, 0u, 0u};
+        wsv[i][j] = in ? ws[j][uint32_t(kb) * uint32_t(N)] : 127u;
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        av[i][t] = in ? *reinterpret_cast<const u32x4*>(a[t] + 64 * s) : u32x4{0u, 0u, 0u, 0u};
+        asv[i][t] = in ? as[t][uint32_t(kb) * uint32_t(M)] : 127u;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[j][t] = mfma_fp4_16(wv[i][j], av[i][t], acc[j][t], wsv[i][j], asv[i][t]);
+  };
+  const int full = (K >> 7) / P;   // whole runs
+#pragma unroll 1
+  for (int s = wave; s < full; s += W) run.template operator()<false>(P * s);
+  if (K % (128 * P) != 0 && full % W == wave) run.template operator()<true>(P * full);
+  // lane (c, g) of tile (j, t): columns n0 + 16 j + 4 g + e of row 16 t + c
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    float wc[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) wc[e] = p.wcscale[min(n0 + 16 * j + 4 * g + e, N - 1)];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][t][e] *= wc[e];
   }
-  // lane (c, g): columns n0 + 4g + e of row 16 t + c
-  float wc[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) wc[e] = p.wcscale[min(n0 + 4 * g + e, N - 1)];
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[t][e] *= wc[e];
 
   // ranks r0 .. r0+31: lane (c, g) supplies ranks r0 + 8g .. +7 of column n
   // (A) and of row m (B)
   for (int r0 = 32 * wave; r0 < R; r0 += 32 * W) {
     const int rr = r0 + 8 * g;
-    uint16_t u[8];
+    u32x4 uv[NT];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = rr + i < R ? p.lora_up[uint32_t(rr + i) * uint32_t(N) + uint32_t(n)] : 0;
-    const u32x4 uv = {bf16_pair(u[0], u[1]), bf16_pair(u[2], u[3]), bf16_pair(u[4], u[5]), bf16_pair(u[6], u[7])};
+    for (int j = 0; j < NT; ++j) {
+      uint16_t u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = rr + i < R ? p.lora_up[uint32_t(rr + i) * uint32_t(N) + uint32_t(n[j])] : 0;
+      uv[j] = u32x4{bf16_pair(u[0], u[1]), bf16_pair(u[2], u[3]), bf16_pair(u[4], u[5]), bf16_pair(u[6], u[7])};
+    }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const uint16_t* la = p.lora_act_in + uint32_t(min(16 * t + c, M - 1)) * uint32_t(R);
@@ -102,21 +137,24 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_few_kernel(const Params 
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = rr + i < R ? la[rr + i] : 0;
       const u32x4 vv = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
-      acc[t] = mfma16<F16>(uv, vv, acc[t]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j][t] = mfma16<F16>(uv[j], vv, acc[j][t]);
     }
   }
 #pragma unroll
-  for (int t = 0; t < MT; ++t) red[(wave * MT + t) * kWave + lane] = acc[t];
-  __syncthreads();
-  for (int t = wave; t < MT; t += W) {
-    f32x4 y = red[t * kWave + lane];
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int q = 1; q < W; ++q) y += red[(q * MT + t) * kWave + lane];
-    const int m = 16 * t + c;
+    for (int t = 0; t < MT; ++t) red[(wave * NT * MT + j * MT + t) * kWave + lane] = acc[j][t];
+  __syncthreads();
+  for (int u = wave; u < NT * MT; u += W) {
+    f32x4 y = red[u * kWave + lane];
+#pragma unroll
+    for (int q = 1; q < W; ++q) y += red[(q * NT * MT + u) * kWave + lane];
+    const int m = 16 * (u % MT) + c;
     if (m >= M) continue;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int col = n0 + 4 * g + e;
+      const int col = n0 + 16 * (u / MT) + 4 * g + e;
       if (col < N) p.out[uint32_t(m) * uint32_t(N) + uint32_t(col)] = narrow<F16>(y[e] + p.bias[col]);
     }
   }
@@ -128,6 +166,16 @@ static bool few_sizes_ok(int M, int N, int K, int R) {
   const int64_t lim = int64_t(1) << 31;
   const int64_t m = M, n = N, k = K, r = R;
   return m * k / 2 < lim && n * k / 2 < lim && m * n * 2 < lim && m * r * 2 < lim && r * n * 2 < lim;
+}
+
+struct FewKernel {
+  const void* fn;
+  int cols, threads;
+};
+
+template <bool F16, class C>
+static FewKernel few_kernel() {
+  return FewKernel{reinterpret_cast<const void*>(mx_few_kernel<F16, C>), C::COLS, C::THREADS};
 }
 
 template <bool F16>
@@ -154,10 +202,16 @@ static int mx_few_run(const uint8_t* act, const uint8_t* ascales, const uint8_t*
   p.K = K;
   p.R = R;
   void* args[] = {&p};
-  const void* k = M <= 16 ? reinterpret_cast<const void*>(mx_few_kernel<F16, 1>)
-                : M <= 32 ? reinterpret_cast<const void*>(mx_few_kernel<F16, 2>)
-                          : reinterpret_cast<const void*>(mx_few_kernel<F16, 4>);
-  const hipError_t e = hipLaunchKernel(k, dim3((N + kFewCols - 1) / kFewCols), dim3(kFewWaves * kWave), args, 0,
+  // Tiling, measured (us): 32 columns a workgroup, which halve the passes over
+  // the activations, where they still fill the chip (64x12288x12288 42.3
+  // against 49.8 with 16; 64x3072x12288 25.8 against 22.8); 16 waves for most
+  // rows and 16 columns (64x3072x12288 19.4 against 22.8); runs of 2 steps for
+  // few rows (1x12288x12288 19.1 against 20.3).
+  const bool wide = N >= 32 * kNumCUs;
+  const FewKernel k = M <= 16 ? few_kernel<F16, FewCfg<1, 1, 8, 2>>()
+                    : M <= 32 ? (wide ? few_kernel<F16, FewCfg<2, 2, 8, 1>>() : few_kernel<F16, FewCfg<2, 1, 8, 1>>())
+                              : (wide ? few_kernel<F16, FewCfg<4, 2, 8, 1>>() : few_kernel<F16, FewCfg<4, 1, 16, 1>>());
+  const hipError_t e = hipLaunchKernel(k.fn, dim3((N + k.cols - 1) / k.cols), dim3(k.threads), args, 0,
                                        static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GEMM_W4A4_OK : GEMM_W4A4_ELAUNCH;
 }
