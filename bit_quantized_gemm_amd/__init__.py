@@ -215,7 +215,7 @@ def _half(t, name):
 
 def _dense(t, name, dtype, shape, device):
     """_check in the order that passes fastest (get_device: the GPU's index, -1 off one)."""
-    if not (t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.get_device() == device.index):
+    if not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == device.index):
         _check(t, name, dtype, shape, device)
 
 
@@ -240,7 +240,7 @@ def _workspace(nbytes, device, stream):
 
 def _call(index, fn, *args):
     """fn(*args) with the device current; raises on a nonzero code."""
-    if _torch.cuda.current_device() == index:
+    if _torch._C._cuda_getDevice() == index:
         rc = fn(*args)
     else:
         with _torch.cuda.device(index):
@@ -282,7 +282,7 @@ def quantize_mxfp4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=No
         else:
             _dense(lora_act_in, "lora_act_in", dtype, (M, R), device)
         ld, la = lora_down.data_ptr(), lora_act_in.data_ptr()
-    lib, index = _native.load(), device.index
+    lib, index = _native.loaded or _native.load(), device.index
     need = lib.quantize_mxfp4_workspace(M, K, R)
     ws = _workspace(need, device, stream) if need > 0 else None
     _call(index, lib.quantize_mxfp4_act_f16 if f16 else lib.quantize_mxfp4_act, x.data_ptr(), ld, act.data_ptr(),
@@ -316,12 +316,19 @@ def gemm_mxfp4_few(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, 
         ascales = ascales.view(u8)
     if wscales.dtype != u8 and wscales.dtype == getattr(torch, "float8_e8m0fnu", None):
         wscales = wscales.view(u8)
-    _dense(act, "act", u8, (M, half), device)
-    _dense(wgt, "wgt", u8, (N, half), device)
-    _dense(ascales, "ascales", u8, (half // 16, M), device)
-    _dense(wscales, "wscales", u8, (half // 16, N), device)
-    _dense(wcscale, "wcscale", f32, (N,), device)
-    _dense(bias, "bias", f32, (N,), device)
+    index = act.get_device()
+    if not (wgt.shape[1] == half and ascales.shape == (half // 16, M) and wscales.shape == (half // 16, N)
+            and wcscale.shape == bias.shape == (N,)
+            and act.dtype is u8 and wgt.dtype is u8 and ascales.dtype is u8 and wscales.dtype is u8
+            and wcscale.dtype is f32 and bias.dtype is f32
+            and act.is_contiguous() and wgt.is_contiguous() and ascales.is_contiguous()
+            and wscales.is_contiguous() and wcscale.is_contiguous() and bias.is_contiguous()
+            and index == wgt.get_device() == ascales.get_device() == wscales.get_device()
+            == wcscale.get_device() == bias.get_device()):
+        for t, name, dt, shape in ((act, "act", u8, (M, half)), (wgt, "wgt", u8, (N, half)),
+                                   (ascales, "ascales", u8, (half // 16, M)), (wscales, "wscales", u8, (half // 16, N)),
+                                   (wcscale, "wcscale", f32, (N,)), (bias, "bias", f32, (N,))):
+            _check(t, name, dt, shape, device)
     if (lora_act_in is None) != (lora_up is None):
         raise ValueError("lora_act_in and lora_up go together")
     R = la = lu = 0
@@ -334,7 +341,7 @@ def gemm_mxfp4_few(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, 
         out = torch.empty((M, N), dtype=dtype, device=device)
     else:
         _dense(out, "out", dtype, (M, N), device)
-    lib, index = _native.load(), device.index
+    lib = _native.loaded or _native.load()
     _call(index, lib.gemm_mxfp4_few_f16 if f16 else lib.gemm_mxfp4_few, act.data_ptr(), ascales.data_ptr(),
           wgt.data_ptr(), wscales.data_ptr(), wcscale.data_ptr(), bias.data_ptr(), la, lu, out.data_ptr(),
           M, N, 2 * half, R, _handle(stream, index))
@@ -388,7 +395,7 @@ def rotary_axes(x, positions, inv_freq, sections, interleaved=True, inverse=Fals
                        *sections, *(0,) * (ROTARY_MAX_AXES - axes), xb, xl, xh, ob, ol, oh, pb, pl,
                        bool(interleaved), bool(inverse), f16)
     index = device.index
-    _call(index, _native.load().rotary_axes, args, _handle(stream, index))
+    _call(index, (_native.loaded or _native.load()).rotary_axes, args, _handle(stream, index))
     return out
 
 
@@ -438,7 +445,7 @@ def cross_attention(q, k, v, kv_lens=None, scale=None, return_lse=False, out=Non
         raise ValueError("the last dimension of q, k, v and out must be dense")
     if scale is None:
         scale = D ** -0.5
-    lib, index = _native.load(), device.index
+    lib, index = _native.loaded or _native.load(), device.index
     rest = (B, LQ, LK, HQ, HKV, D, qb, ql, qh, kb, kl, kh, vb, vl, vh, ob, ol, oh, scale, f16)
     args = ATTENTION_PACK(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), l, lens, *rest, 0, 0)
     need = lib.cross_attention_workspace(args)

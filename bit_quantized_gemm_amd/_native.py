@@ -76,6 +76,7 @@ class Plan(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+loaded = None   # the library once load() has returned it, for callers that count microseconds
 
 
 def library_path() -> str:
@@ -84,7 +85,7 @@ def library_path() -> str:
 
 def load() -> ctypes.CDLL:
     """Load libgemm_w4a4.so (once). Raises if it has not been built."""
-    global _lib
+    global _lib, loaded
     with _lock:
         if _lib is not None:
             return _lib
@@ -140,7 +141,7 @@ def load() -> ctypes.CDLL:
         lib.cross_attention_workspace.restype = i64
         lib.gemm_w4a4_strerror.argtypes = [i]
         lib.gemm_w4a4_strerror.restype = ctypes.c_char_p
-        _lib = lib
+        _lib = loaded = lib
         return lib
 
 
