@@ -54,6 +54,23 @@ def test_lengths(LQ, D, HQ, HKV, dtype):
     check(q, k, v, lens, dtype, f"lengths LQ={LQ}")
 
 
+@pytest.mark.parametrize("B,HQ,HKV,LK", [(100, 2, 1, 700), (65, 3, 3, 520), (2, 8, 4, 6000), (7, 6, 2, 3000)])
+@pytest.mark.parametrize("shape", ["falling", "one long", "random", "mostly empty"])
+def test_uneven_sequences_of_one_token(B, HQ, HKV, LK, shape):
+    """Sequences of very different lengths, whose keys are cut into parts of even length:
+    every key is counted once, whatever the lengths."""
+    rng = np.random.default_rng(B + LK)
+    lens = {"falling": [LK * (B - b) // B for b in range(B)], "one long": [3] * (B - 1) + [LK],
+            "random": [int(n) for n in rng.integers(0, LK + 1, B)],
+            "mostly empty": [0 if b != B // 2 else LK for b in range(B)]}[shape]
+    q, k, v = inputs(rng, B, 1, LK, HQ, HKV, 32, "f16")
+    out, _ = check(q, k, v, lens, "f16", f"{B} {shape}")
+    # counting: with equal keys the result is the mean of the values in use
+    same = np.repeat(k[:1, :1], LK, 1).repeat(B, 0)
+    count = half_bits(np.ones((B, LK, HKV, 32)) * (np.arange(LK) % 2)[None, :, None, None], "f16")
+    check(q, same, count, lens, "f16", f"{B} {shape} counted")
+
+
 @pytest.mark.parametrize("LQ", [1, 200])
 def test_all_lengths_zero_and_no_keys(LQ):
     q = to_dev(normal_bits(np.random.default_rng(1), (2, LQ, 4, 64), "bf16"), "bf16")
