@@ -19,8 +19,8 @@ in the library's HIP kernels. If the library is missing the calls raise.
 from __future__ import annotations
 
 from . import _native
-from ._native import (ATTENTION_MAX_HEAD_DIM, ATTENTION_PACK, FEW_MAX_M, ROTARY_MAX_AXES, ROTARY_MAX_HEAD_DIM,
-                      ROTARY_PACK, AttentionArgs, RotaryArgs,
+from ._native import (ATTENTION_MAX_HEAD_DIM, FEW_MAX_M, ROTARY_MAX_AXES, ROTARY_MAX_HEAD_DIM,
+                      AttentionArgs, RotaryArgs,
                       cross_attention_raw, cross_attention_workspace, gemm_mxfp4_few_raw, quantize_mxfp4_raw,
                       quantize_mxfp4_workspace, rotary_axes_raw)
 from ._native import (EALIGN, EDEVICE, EINVAL, ENOMEM, ESCRATCH, ELAUNCH, EOVERLAP, FORMATS, MAX_R, OK, QUANTIZE_MAX_R,
@@ -183,70 +183,23 @@ def quantize_w4a4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=Non
 
 # ---------------------------------------------------------------- operators around the layers
 #
-# Their small calls are bound by this binding, not by the GPU, so it does each
-# check once, on plain attributes, and takes the stream's handle without making
-# a stream object (a call of four vectors through quantize_mxfp4_act went from
-# 19.5 to QV us, one vector through gemm_mxfp4_few from 15.2 to FV).
-
-_torch = None
-_HALF = {}
+# Checks, allocation and the call are one native step (csrc/torch_binding.cpp).
 
 
-def _bind():
-    """torch, imported at the first call that needs it."""
-    global _torch
-    import torch
-    _HALF.update({torch.bfloat16: False, torch.float16: True})
-    _torch = torch
-    return torch
-
-
-def _half(t, name):
-    """Whether a 16-bit floating tensor on a GPU is binary16 (else bfloat16)."""
-    if _torch is None:
-        _bind()
-    f16 = _HALF.get(t.dtype)
-    if f16 is None:
-        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a GPU device")
-    return f16
-
-
-def _dense(t, name, dtype, shape, device):
-    """_check in the order that passes fastest (get_device: the GPU's index, -1 off one)."""
-    if not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == device.index):
-        _check(t, name, dtype, shape, device)
-
-
-def _handle(stream, index):
-    """The HIP stream of a call: `stream`, else torch's current one on that device."""
+def _run(name, stream, *args):
+    """The native function `name` on torch's current stream, or with `stream` current."""
+    fn = getattr(_native.binding(), name)
     if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _workspace(nbytes, device, stream):
-    """nbytes of device memory for a call on `stream` (None: torch's current one).
-    The allocator hands memory out again in the order of the stream it was asked for."""
-    torch = _torch
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-
-
-def _call(index, fn, *args):
-    """fn(*args) with the device current; raises on a nonzero code."""
-    if _torch._C._cuda_getDevice() == index:
-        rc = fn(*args)
+        r = fn(*args)
     else:
-        with _torch.cuda.device(index):
-            rc = fn(*args)
-    if rc != OK:
-        raise GemmError(rc)
+        import torch
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=args[0].device)
+        with torch.cuda.stream(stream):
+            r = fn(*args)
+    if type(r) is int:
+        raise GemmError(r)
+    return r
 
 
 def quantize_mxfp4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=None, stream=None):
@@ -256,38 +209,7 @@ def quantize_mxfp4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=No
     given, lora_act_in [M, R] = x @ lora_down^T of that type. Without lora_down
     it also lays out weights [N, K]. Outputs are allocated when None.
     Returns (act, ascales, lora_act_in or None)."""
-    f16 = _half(x, "x")
-    torch, device, dtype = _torch, x.device, x.dtype
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D")
-    M, K = x.shape
-    if not x.is_contiguous():
-        raise ValueError("x must be contiguous")
-    R = ld = la = 0
-    if lora_down is not None:
-        R = lora_down.shape[0]
-        _dense(lora_down, "lora_down", dtype, (R, K), device)
-    u8 = torch.uint8
-    if act is None:
-        act = torch.empty((M, K // 2), dtype=u8, device=device)
-    else:
-        _dense(act, "act", u8, (M, K // 2), device)
-    if ascales is None:
-        ascales = torch.empty((K // 32, M), dtype=u8, device=device)
-    else:
-        _dense(ascales, "ascales", u8, (K // 32, M), device)
-    if R > 0:
-        if lora_act_in is None:
-            lora_act_in = torch.empty((M, R), dtype=dtype, device=device)
-        else:
-            _dense(lora_act_in, "lora_act_in", dtype, (M, R), device)
-        ld, la = lora_down.data_ptr(), lora_act_in.data_ptr()
-    lib, index = _native.loaded or _native.load(), device.index
-    need = lib.quantize_mxfp4_workspace(M, K, R)
-    ws = _workspace(need, device, stream) if need > 0 else None
-    _call(index, lib.quantize_mxfp4_act_f16 if f16 else lib.quantize_mxfp4_act, x.data_ptr(), ld, act.data_ptr(),
-          ascales.data_ptr(), la, M, K, R, 0 if ws is None else ws.data_ptr(), need, _handle(stream, index))
-    return act, ascales, (lora_act_in if R else None)
+    return _run("quantize_mxfp4_act", stream, x, lora_down, act, ascales, lora_act_in)
 
 
 def gemm_mxfp4_few(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, lora_up=None,
@@ -295,57 +217,7 @@ def gemm_mxfp4_few(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, 
     """Enqueue the fused MXFP4 operator for few rows (M <= FEW_MAX_M): arguments
     and result as gemm_mxfp4, in a kernel that streams the weights once.
     """
-    if dtype is None:
-        given = out if out is not None else lora_act_in
-        if given is not None:
-            dtype = given.dtype
-    torch = _torch or _bind()
-    if dtype is None:
-        dtype = torch.bfloat16
-    f16 = _HALF.get(dtype)
-    if f16 is None:
-        raise TypeError(f"the LoRA/output type must be bfloat16 or float16, got {dtype}")
-    if not act.is_cuda:
-        raise ValueError("tensors must live on a GPU device")
-    if act.dim() != 2 or wgt.dim() != 2:
-        raise ValueError("act and wgt must be 2-D")
-    device, u8, f32 = act.device, torch.uint8, torch.float32
-    M, half = act.shape
-    N = wgt.shape[0]
-    if ascales.dtype != u8 and ascales.dtype == getattr(torch, "float8_e8m0fnu", None):
-        ascales = ascales.view(u8)
-    if wscales.dtype != u8 and wscales.dtype == getattr(torch, "float8_e8m0fnu", None):
-        wscales = wscales.view(u8)
-    index = act.get_device()
-    if not (wgt.shape[1] == half and ascales.shape == (half // 16, M) and wscales.shape == (half // 16, N)
-            and wcscale.shape == bias.shape == (N,)
-            and act.dtype is u8 and wgt.dtype is u8 and ascales.dtype is u8 and wscales.dtype is u8
-            and wcscale.dtype is f32 and bias.dtype is f32
-            and act.is_contiguous() and wgt.is_contiguous() and ascales.is_contiguous()
-            and wscales.is_contiguous() and wcscale.is_contiguous() and bias.is_contiguous()
-            and index == wgt.get_device() == ascales.get_device() == wscales.get_device()
-            == wcscale.get_device() == bias.get_device()):
-        for t, name, dt, shape in ((act, "act", u8, (M, half)), (wgt, "wgt", u8, (N, half)),
-                                   (ascales, "ascales", u8, (half // 16, M)), (wscales, "wscales", u8, (half // 16, N)),
-                                   (wcscale, "wcscale", f32, (N,)), (bias, "bias", f32, (N,))):
-            _check(t, name, dt, shape, device)
-    if (lora_act_in is None) != (lora_up is None):
-        raise ValueError("lora_act_in and lora_up go together")
-    R = la = lu = 0
-    if lora_act_in is not None:
-        R = lora_act_in.shape[1]
-        _dense(lora_act_in, "lora_act_in", dtype, (M, R), device)
-        _dense(lora_up, "lora_up", dtype, (R, N), device)
-        la, lu = lora_act_in.data_ptr(), lora_up.data_ptr()
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=device)
-    else:
-        _dense(out, "out", dtype, (M, N), device)
-    lib = _native.loaded or _native.load()
-    _call(index, lib.gemm_mxfp4_few_f16 if f16 else lib.gemm_mxfp4_few, act.data_ptr(), ascales.data_ptr(),
-          wgt.data_ptr(), wscales.data_ptr(), wcscale.data_ptr(), bias.data_ptr(), la, lu, out.data_ptr(),
-          M, N, 2 * half, R, _handle(stream, index))
-    return out
+    return _run("gemm_mxfp4_few", stream, act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out, dtype)
 
 
 def rotary_axes(x, positions, inv_freq, sections, interleaved=True, inverse=False, out=None, stream=None):
@@ -361,42 +233,7 @@ def rotary_axes(x, positions, inv_freq, sections, interleaved=True, inverse=Fals
     of x from the gradient of the result. out: allocated (dense) when None; x
     itself for in place. Returns out.
     """
-    f16 = _half(x, "x")
-    torch, device = _torch, x.device
-    if x.dim() != 4:
-        raise ValueError("x must be [batch, tokens, heads, head_dim]")
-    shape = x.shape
-    B, L, H, D = shape
-    axes, pairs = len(sections), sum(sections)
-    if not 1 <= axes <= ROTARY_MAX_AXES:
-        raise ValueError(f"1 to {ROTARY_MAX_AXES} axes, got {axes}")
-    if positions.dtype != torch.int32 or inv_freq.dtype != torch.float32:
-        raise TypeError("positions must be int32 and inv_freq float32")
-    ps = positions.stride()
-    if positions.shape == (B, L, axes):
-        pb, pl = ps[0], ps[1]
-    elif positions.shape == (L, axes):
-        pb, pl = 0, ps[0]
-    else:
-        raise ValueError(f"positions must be [{B}, {L}, {axes}] or [{L}, {axes}], got {tuple(positions.shape)}")
-    if inv_freq.shape != (pairs,) or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be contiguous, one value per pair")
-    if positions.device != device or inv_freq.device != device:
-        raise ValueError(f"positions and inv_freq must be on {device}")
-    xb, xl, xh, xd = x.stride()
-    if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=device)
-    elif out.dtype != x.dtype or out.shape != shape or out.device != device:
-        raise ValueError("out must have x's type, shape and device")
-    ob, ol, oh, od = out.stride()
-    if (axes > 1 and ps[-1] != 1) or (D > 1 and (xd != 1 or od != 1)):
-        raise ValueError("the last dimension of x, out and positions must be dense")
-    args = ROTARY_PACK(x.data_ptr(), out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), B, L, H, D, axes,
-                       *sections, *(0,) * (ROTARY_MAX_AXES - axes), xb, xl, xh, ob, ol, oh, pb, pl,
-                       bool(interleaved), bool(inverse), f16)
-    index = device.index
-    _call(index, (_native.loaded or _native.load()).rotary_axes, args, _handle(stream, index))
-    return out
+    return _run("rotary_axes", stream, x, positions, inv_freq, sections, interleaved, inverse, out)
 
 
 def cross_attention(q, k, v, kv_lens=None, scale=None, return_lse=False, out=None, stream=None):
@@ -412,45 +249,4 @@ def cross_attention(q, k, v, kv_lens=None, scale=None, return_lse=False, out=Non
     dense when None), and with return_lse also the float32 log-sum-exp
     [batch, q_heads, q_len] (-inf for rows without keys).
     """
-    f16 = _half(q, "q")
-    torch, device, dtype = _torch, q.device, q.dtype
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q, k and v must be 4-D")
-    shape, kshape = q.shape, k.shape
-    B, LQ, HQ, D = shape
-    LK, HKV = kshape[1], kshape[2]
-    if kshape[0] != B or kshape[3] != D or v.shape != kshape:
-        raise ValueError(f"k and v must be [{B}, kv_len, kv_heads, {D}], got {tuple(kshape)} and {tuple(v.shape)}")
-    if k.dtype != dtype or v.dtype != dtype:
-        raise TypeError(f"k and v must be {dtype}, got {k.dtype} and {v.dtype}")
-    if k.device != device or v.device != device:
-        raise ValueError(f"k and v must be on {device}")
-    lens = l = 0
-    if kv_lens is not None:
-        _dense(kv_lens, "kv_lens", torch.int32, (B,), device)
-        lens = kv_lens.data_ptr()
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-    elif out.dtype != dtype or out.shape != shape or out.device != device:
-        raise ValueError("out must have q's type, shape and device")
-    lse = None
-    if return_lse:
-        lse = torch.empty((B, HQ, LQ), dtype=torch.float32, device=device)
-        l = lse.data_ptr()
-    qb, ql, qh, qd = q.stride()
-    kb, kl, kh, kd = k.stride()
-    vb, vl, vh, vd = v.stride()
-    ob, ol, oh, od = out.stride()
-    if D > 1 and not qd == kd == vd == od == 1:
-        raise ValueError("the last dimension of q, k, v and out must be dense")
-    if scale is None:
-        scale = D ** -0.5
-    lib, index = _native.loaded or _native.load(), device.index
-    rest = (B, LQ, LK, HQ, HKV, D, qb, ql, qh, kb, kl, kh, vb, vl, vh, ob, ol, oh, scale, f16)
-    args = ATTENTION_PACK(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), l, lens, *rest, 0, 0)
-    need = lib.cross_attention_workspace(args)
-    if need > 0:
-        ws = _workspace(need, device, stream)
-        args = ATTENTION_PACK(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), l, lens, *rest, ws.data_ptr(), need)
-    _call(index, lib.cross_attention, args, _handle(stream, index))
-    return (out, lse) if return_lse else out
+    return _run("cross_attention", stream, q, k, v, kv_lens, scale, return_lse, out)

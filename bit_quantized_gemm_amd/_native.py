@@ -7,11 +7,12 @@ missing, loading fails loudly.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 
-from .build import LIB_PATH
+from .build import BINDING_PATH, LIB_PATH
 
 OK = 0
 EINVAL = -1
@@ -61,12 +62,6 @@ class AttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_int64)]
 
 
-# The same structures as bytes in one step (building a ctypes one costs a
-# microsecond more), in the order of their fields, "x" where a C compiler pads.
-ROTARY_PACK = struct.Struct("4P9i4x8q3i4x").pack
-ATTENTION_PACK = struct.Struct("6P6i12qfiPq").pack
-
-
 class Plan(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int) for f in _PLAN_FIELDS]
 
@@ -76,7 +71,7 @@ class Plan(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
-loaded = None   # the library once load() has returned it, for callers that count microseconds
+_binding = None
 
 
 def library_path() -> str:
@@ -85,7 +80,7 @@ def library_path() -> str:
 
 def load() -> ctypes.CDLL:
     """Load libgemm_w4a4.so (once). Raises if it has not been built."""
-    global _lib, loaded
+    global _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -141,8 +136,26 @@ def load() -> ctypes.CDLL:
         lib.cross_attention_workspace.restype = i64
         lib.gemm_w4a4_strerror.argtypes = [i]
         lib.gemm_w4a4_strerror.restype = ctypes.c_char_p
-        _lib = loaded = lib
+        _lib = lib
         return lib
+
+
+def binding():
+    """The native part of the binding, _torch_binding.so (loaded once, after torch and
+    the library). Raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        import torch  # noqa: F401
+        load()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                f"{BINDING_PATH} is missing: build it first (python -m bit_quantized_gemm_amd.build "
+                "or __graft_entry__.build()); there is no other path to these operators")
+        loader = importlib.machinery.ExtensionFileLoader("_torch_binding", BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("_torch_binding", BINDING_PATH, loader=loader)
+        _binding = importlib.util.module_from_spec(spec)
+        loader.exec_module(_binding)
+    return _binding
 
 
 def strerror(code: int) -> str:

@@ -4,7 +4,8 @@
 
 writes bit_quantized_gemm_amd/libgemm_w4a4.so (the operator: include/gemm_w4a4.h)
 and bit_quantized_gemm_amd/libw4a4_probes.so (measurement aids:
-include/w4a4_probes.h). The kernels are compiled for gfx950 only, with
+include/w4a4_probes.h), and bit_quantized_gemm_amd/_torch_binding.so (the native
+part of the Python binding, host code over torch's C++ interface). The kernels are compiled for gfx950 only, with
 packed-fp32 VALU instructions disabled.
 
 Each source is compiled to an object first (in parallel). For the operator
@@ -36,6 +37,7 @@ LIBS = {
                 "mxfp4_few.hip", "rotary.hip", "attention.hip"), True),
     PROBES_LIB_PATH: (("mfma_peak.hip", "route_probe.hip"), False),
 }
+BINDING_PATH = os.path.join(PKG_DIR, "_torch_binding.so")
 ARCH = "gfx950"
 LLVM = "/opt/rocm/llvm/bin"
 
@@ -155,15 +157,29 @@ def _build_one(path: str, sources, with_resources: bool, verbose: bool) -> None:
     os.replace(tmp, path)
 
 
+def _build_binding(verbose: bool) -> None:
+    """The torch binding over the operator library (g++, host code; found beside the library at run time)."""
+    import sysconfig
+
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = BINDING_PATH + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-I{INCLUDE}",
+          f"-I{sysconfig.get_paths()['include']}"] + [f"-isystem{p}" for p in include_paths()] +
+         [os.path.join(CSRC, "torch_binding.cpp"), "-o", tmp, f"-L{PKG_DIR}", "-lgemm_w4a4", "-Wl,-rpath,$ORIGIN"] +
+         [f"-L{p}" for p in library_paths()] + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"], verbose)
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(verbose: bool = False) -> str:
     """Compile every HIP source into the in-tree shared libraries; returns the
     operator library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     for path, (sources, with_res) in LIBS.items():
         _build_one(path, sources, with_res, verbose)
+    _build_binding(verbose)
     return LIB_PATH
 
 
 if __name__ == "__main__":
     build(verbose=True)
-    print("\n".join(LIBS))
+    print("\n".join(list(LIBS) + [BINDING_PATH]))

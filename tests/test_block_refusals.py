@@ -197,10 +197,3 @@ def test_structures_match_the_header(tmp_path):
         want += [ctypes.sizeof(c)] + [getattr(c, f[0]).offset for f in c._fields_]
     assert got == want
 
-
-def test_packed_structures_match():
-    """The binding's packed bytes are the ctypes structures' bytes."""
-    r = w4.RotaryArgs(1, 2, 3, 4, 5, 6, 7, 8, 3, (9, 10, 11, 0), (12, 13, 14), (15, 16, 17), (18, 19), 1, 0, 1)
-    assert w4._native.ROTARY_PACK(1, 2, 3, 4, 5, 6, 7, 8, 3, 9, 10, 11, 0, 12, 13, 14, 15, 16, 17, 18, 19, True, False, True) == bytes(r)
-    a = w4.AttentionArgs(*range(1, 13), (13, 14, 15), (16, 17, 18), (19, 20, 21), (22, 23, 24), 0.5, 1, 26, 27)
-    assert w4._native.ATTENTION_PACK(*range(1, 25), 0.5, True, 26, 27) == bytes(a)
