@@ -6,7 +6,9 @@
 // in the layout of the LoRA product's A operand: lane (r, g) of a wave holds row
 // r, k = 32 i + 8 g .. + 7 for the four blocks i of a 128-wide span, so that
 // four lanes read 64 neighbouring bytes (one whole block a lane, 64 bytes
-// apart, cost four times the cache cycles: 14.2 us at 4096 x 3072, R = 32).
+// apart, cost four times the cache cycles). 4096 x 3072, R = 32: 11.9 us, 2.7
+// TB/s (14.2 with a block a lane); past the floor it is the reading of lora_down,
+// 294 KB a compute unit, that bounds it. 1001 x 12288, R = 128: 18.9 us.
 // A block's largest magnitude meets over its four lanes by lane swaps, and so
 // do its codes, which leave as 16 bytes a lane.
 //
@@ -44,6 +46,7 @@ struct MxProdParams {
   float* part;          // ks > 1 and R > 0: [slice][M][R] float32 sums
   int M, K, R;
   int ks, sps;          // K slices, spans per slice
+  int groups;           // workgroups that share rows and slice, a rank tile each
 };
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
@@ -123,7 +126,9 @@ __device__ __forceinline__ uint32_t quantize_span(const u32x4 (&d)[4], int g, u3
 
 constexpr int kMxProdWaves = 8;
 
-// One workgroup a 16 rows. RT: rank tiles of 16 (0: no LoRA product).
+// A workgroup a 16 rows, or one for each of `groups` rank tiles of them, of
+// which the first writes the codes. RT: rank tiles of a workgroup, 0 (no LoRA
+// product) to 2.
 template <bool F16, int RT>
 __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const MxProdParams p) {
   constexpr int W = kMxProdWaves, NA = RT > 0 ? RT : 1;
@@ -132,7 +137,8 @@ __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int M = p.M, K = p.K, R = p.R;
-  const int rb = blockIdx.x / p.ks, z = blockIdx.x - rb * p.ks;
+  const int q0 = blockIdx.x % p.groups, blk = blockIdx.x / p.groups;
+  const int rb = blk / p.ks, z = blk - rb * p.ks;
   const int m0 = rb * 16;
   const int nsp = (K + 127) / 128;
   const int s_end = min(nsp, (z + 1) * p.sps);
@@ -142,52 +148,38 @@ __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const
   const uint16_t* lr[NA];
 #pragma unroll
   for (int j = 0; j < RT; ++j)   // ranks past R repeat the last; their sums are not stored
-    lr[j] = p.lora_down + size_t(min(16 * j + r, R - 1)) * size_t(K) + 8 * g;
+    lr[j] = p.lora_down + size_t(min(16 * (q0 + j) + r, R - 1)) * size_t(K) + 8 * g;
   f32x4 acc[NA];
 #pragma unroll
   for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // A span's x, and its lora_down operands where they are few, are asked for
-  // one span ahead; many operands in halves, the first before the codes are
-  // worked out. TAIL: the span that K ends in; its blocks past K (K % 32 == 0: in
-  // or out whole) read as zeros.
-  constexpr bool AHEAD = RT <= 2;
-  constexpr int NB = RT > 4 ? 2 : 4;   // k-steps of operands held
-  u32x4 x[2][4], b[2][NB][NA];
+  // A span's x and lora_down operands are asked for one span ahead. TAIL: the
+  // span that K ends in; its blocks past K (K % 32 == 0: in or out whole) read
+  // as zeros.
+  u32x4 x[2][4], b[2][4][NA];
   auto load = [&]<bool TAIL>(const uint16_t* from, int k) __attribute__((always_inline)) {
     return !TAIL || k < K ? *reinterpret_cast<const u32x4*>(from + k) : u32x4{0u, 0u, 0u, 0u};
-  };
-  auto load_b = [&]<bool TAIL>(u32x4 (&bs)[NB][NA], int s, int i0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) bs[i][j] = load.template operator()<TAIL>(lr[j], s * 128 + 32 * (i0 + i));
-  };
-  auto products = [&](const u32x4 (&d)[4], const u32x4 (&bs)[NB][NA], int i0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[j] = mfma16<F16>(d[i0 + i], bs[i][j], acc[j]);
   };
   auto ask = [&]<bool TAIL>(int q, int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[q][i] = load.template operator()<TAIL>(xr, s * 128 + 32 * i);
-    if constexpr (AHEAD) load_b.template operator()<TAIL>(b[q], s, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) b[q][i][j] = load.template operator()<TAIL>(lr[j], s * 128 + 32 * i);
   };
   auto work = [&]<bool TAIL>(int q, int s) __attribute__((always_inline)) {
-    if constexpr (!AHEAD) load_b.template operator()<TAIL>(b[q], s, 0);
     const int k = s * 128 + 32 * g;
     u32x4 codes;
     const uint32_t byte = quantize_span<F16>(x[q], g, codes);
-    if (live && (!TAIL || k < K)) {
+    if (live && q0 == 0 && (!TAIL || k < K)) {
       *reinterpret_cast<u32x4*>(p.act + size_t(row) * size_t(K / 2) + k / 2) = codes;
       p.ascales[size_t(k / 32) * size_t(M) + row] = uint8_t(byte);
     }
-    products(x[q], b[q], 0);
-    if constexpr (NB == 2) {
-      load_b.template operator()<TAIL>(b[q], s, 2);
-      products(x[q], b[q], 2);
-    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) acc[j] = mfma16<F16>(x[q][i], b[q][i][j], acc[j]);
   };
   const int e = min(s_end, K / 128);   // past the whole spans
   int s = z * p.sps + wave;
@@ -212,7 +204,7 @@ __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const
       f32x4 sum = red[j * kWave + lane];
 #pragma unroll
       for (int w = 1; w < W; ++w) sum += red[(w * RT + j) * kWave + lane];
-      const int rank = 16 * j + r;
+      const int rank = 16 * (q0 + j) + r;
       if (rank >= R) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -382,6 +374,7 @@ struct MxProdPlan {
   int threads;
   int rbs;       // row blocks
   int ks, sps;   // K slices, spans of a slice
+  int groups;    // rank tiles apart, a workgroup each
   int64_t bytes;
 };
 
@@ -404,6 +397,11 @@ static MxProdPlan mx_prod_plan(int M, int K, int R) {
   const int ks = std::max(1, std::min(nsp / (pl.shared ? 3 : 2 * waves), mx_cus() / pl.rbs));
   pl.sps = (nsp + ks - 1) / ks;
   pl.ks = (nsp + pl.sps - 1) / pl.sps;
+  // A workgroup for each rank tile where that leaves no compute unit with two of
+  // them, and for up to 16 rows: one unit takes 2.6 us to fetch a rank tile of
+  // 3072 k (4x3072 R=32: 8.3 us with both tiles in one workgroup, 6.0 apart).
+  const int tiles = (R + 15) / 16;
+  pl.groups = !pl.shared && tiles > 1 && (M <= 16 || int64_t(pl.rbs) * pl.ks * tiles <= mx_cus()) ? tiles : 1;
   pl.bytes = pl.ks > 1 && R > 0 ? int64_t(pl.ks) * M * R * 4 : 0;
   return pl;
 }
@@ -415,17 +413,15 @@ static bool mx_prod_sizes_ok(int M, int K, int R) {
 }
 
 template <bool F16>
-static const void* mx_producer_of(int R, int shared) {
+static const void* mx_producer_of(int R, int shared, int groups) {
   if (shared == 8) return reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<8, 8>>);
   if (shared)
     return R <= 32 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<2, 4>>)
          : R <= 64 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<4, 4>>)
                    : reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<8, 4>>);
   if (R == 0) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 0>);
-  if (R <= 16) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 1>);
-  if (R <= 32) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 2>);
-  if (R <= 64) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 4>);
-  return reinterpret_cast<const void*>(mx_producer_kernel<F16, 8>);
+  if (R <= 16 || groups > 1) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 1>);
+  return reinterpret_cast<const void*>(mx_producer_kernel<F16, 2>);
 }
 
 template <bool F16>
@@ -454,10 +450,12 @@ static int mx_quantize_run(const uint16_t* x, const uint16_t* lora_down, uint8_t
   }
   const int dev_rc = check_device();
   if (dev_rc != GEMM_W4A4_OK) return dev_rc;
-  MxProdParams p{x, lora_down, act, ascales, lora_act_in, static_cast<float*>(workspace), M, K, R, pl.ks, pl.sps};
+  MxProdParams p{x, lora_down, act, ascales, lora_act_in, static_cast<float*>(workspace),
+                 M, K, R, pl.ks, pl.sps, pl.groups};
   void* args[] = {&p};
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  hipError_t e = hipLaunchKernel(mx_producer_of<F16>(R, pl.shared), dim3(unsigned(pl.rbs) * unsigned(pl.ks)),
+  hipError_t e = hipLaunchKernel(mx_producer_of<F16>(R, pl.shared, pl.groups),
+                                 dim3(unsigned(pl.rbs) * unsigned(pl.ks) * unsigned(pl.groups)),
                                  dim3(pl.threads), args, 0, st);
   if (e == hipSuccess && pl.bytes > 0)
     e = hipLaunchKernel(reinterpret_cast<const void*>(mx_producer_join_kernel<F16>),
