@@ -48,13 +48,15 @@ enum {
                                  or any tensor of 2^31 bytes or more) or a required
                                  NULL pointer */
   GEMM_W4A4_EALIGN = -2,      /* act/wgt not 16-byte aligned, wcscale/bias not 4-byte,
-                                 lora/out not 2-byte aligned */
+                                 lora/out not 2-byte aligned; other entry points: as stated
+                                 with them */
   GEMM_W4A4_ELAUNCH = -3,     /* the HIP launch itself failed */
-  GEMM_W4A4_EOVERLAP = -4,    /* out overlaps an input */
+  GEMM_W4A4_EOVERLAP = -4,    /* an output overlaps an input or another output */
   GEMM_W4A4_EDEVICE = -5,     /* the current device is not gfx950 */
   GEMM_W4A4_ENOMEM = -6,      /* quantize_w4a4_act could not allocate its scratch buffer */
   GEMM_W4A4_ESCRATCH = -7     /* the call needs more scratch than quantize_w4a4_act_noalloc's
-                                 fixed array (QUANTIZE_W4A4_NOALLOC_SCRATCH_BYTES) */
+                                 fixed array (QUANTIZE_W4A4_NOALLOC_SCRATCH_BYTES), or than
+                                 the workspace that the caller gave */
 };
 
 #define GEMM_W4A4_MAX_R 1024
@@ -449,8 +451,8 @@ int rotary_axes(const rotary_axes_t* args, void* stream);
  * sums are float32; the weights exp(...) are rounded to the 16-bit type for
  * the product with v.
  *
- * scale: positive, at most 1e30. head_dim: a multiple of 8, 8 .. CROSS_ATTENTION_MAX_HEAD_DIM; q_heads a
- * multiple of kv_heads. Strides in elements, multiples of 8 (a dimension of
+ * scale: positive, at most 1e30. head_dim: a multiple of 8, 8 ..
+ * CROSS_ATTENTION_MAX_HEAD_DIM; q_heads a multiple of kv_heads. Strides in elements, multiples of 8 (a dimension of
  * size 1 excepted), non-negative, k's and v's token strides below 2^23; the
  * last dimension is dense; all four tensors 16-byte aligned. q, k and v may
  * repeat memory (stride 0); out may not (GEMM_W4A4_EINVAL) and out and lse may
@@ -482,8 +484,8 @@ typedef struct {
   int64_t workspace_bytes;
 } cross_attention_t;
 int cross_attention(const cross_attention_t* args, void* stream);
-/* Workspace bytes of this call on the current device (sizes only; no pointer is
- * read), or GEMM_W4A4_EINVAL (host only). */
+/* Workspace bytes of this call on the current device (sizes and strides only; no
+ * pointer is read), or GEMM_W4A4_EINVAL (host only). */
 int64_t cross_attention_workspace(const cross_attention_t* args);
 
 /* Static string for a return code (never NULL). */

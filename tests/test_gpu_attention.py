@@ -133,6 +133,29 @@ def test_strides(LQ):
     check(q, np.repeat(k[:1], B, 0), np.repeat(v[:1], B, 0), None, "bf16", "repeated", dev=[to_dev(q, "bf16")] + one)
 
 
+@pytest.mark.parametrize("LQ", [1, 40, 300])
+@pytest.mark.parametrize("LK,step", [(1, 0), (5, 0), (45, 0), (700, 0), (45, 8), (300, 8)])
+def test_keys_that_share_memory(LQ, LK, step):
+    """One key for all positions (stride 0) and rows that overlap (stride 8): positions past the
+    length are not in the sums, with infinities among the values too, which 0 times would be NaN."""
+    print(f"case: {LQ} {LK} {step}", flush=True)
+    rng = np.random.default_rng(LQ + LK)
+    D = 64
+    q = normal_bits(rng, (2, LQ, 2, D), "f16")
+    flat = [normal_bits(rng, (2, LK * step + D), "f16") for _ in range(2)]
+    dev = [to_dev(t, "f16").as_strided((2, LK, 1, D), (t.shape[1], step, D, 1)) for t in flat]
+    k, v = (np.stack([np.stack([t[b, i * step:i * step + D] for i in range(LK)]) for b in range(2)])[:, :, None] for t in flat)
+    lens = [LK, LK - LK // 3]
+    check(q, k, v, lens, "f16", f"stride {step}", dev=[to_dev(q, "f16"), *dev])
+    for t, host in zip(flat[1], v):      # the first position's first value: infinite
+        t[0] = host[0, 0, 0] = 0x7C00
+        for i in range(1, LK if step == 0 else 1):
+            host[i, 0, 0] = 0x7C00
+    vd = to_dev(flat[1], "f16").as_strided((2, LK, 1, D), (flat[1].shape[1], step, D, 1))
+    out = w4.cross_attention(to_dev(q, "f16"), dev[0], vd, kv_lens=torch.tensor(lens, dtype=torch.int32, device=DEV))
+    assert torch.isposinf(out[..., 0]).all() and torch.isfinite(out[..., 1:]).all()
+
+
 def test_parts_join():
     """Attention over two parts of the keys joined by their log-sum-exps is attention over all."""
     rng = np.random.default_rng(5)
