@@ -233,10 +233,10 @@ struct MxShared {
   static constexpr int XTILE = 16 * 256;              // a span of a wave's x, 4 loads
   static constexpr int XOFF = RING * TILE;
   static constexpr int LDS = XOFF + W * 2 * XTILE;
-  // loads of the span after the one that is needed (the stores of codes among
-  // them only make the wait longer)
+  // What a wave has asked for after the loads of the span that is needed: the
+  // loads of the next span, and past the first span two stores of codes, or four.
   static constexpr int YOUNGER = LOADS + 4;
-  static_assert(RT * 4 % W == 0 && LDS <= kLdsLimit && YOUNGER < 64, "LDS and wait counter");
+  static_assert(RT * 4 % W == 0 && LDS <= kLdsLimit && YOUNGER + 2 < 64, "LDS and wait counter");
 };
 
 template <bool F16, class C>
@@ -291,6 +291,9 @@ __global__ __launch_bounds__(C::W * kWave) void mx_producer_shared_kernel(const 
   for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const bool live = mw + r < M;
   const int row = min(mw + r, M - 1);
+  const uint32_t act_row = uint32_t(row) * (uint32_t(K) / 2u);
+  const auto act = __builtin_amdgcn_make_buffer_rsrc(p.act, 0, int(uint32_t(M) * (uint32_t(K) / 2u)), 0x00020000);
+  const auto ascales = __builtin_amdgcn_make_buffer_rsrc(p.ascales, 0, int(uint32_t(K / 32) * uint32_t(M)), 0x00020000);
 
   ask_x(s_beg, 0);
   ask_l(s_beg, 0);
@@ -298,7 +301,8 @@ __global__ __launch_bounds__(C::W * kWave) void mx_producer_shared_kernel(const 
   ask_l(s_beg + 1, 1);
   int place = 0;   // of the span in the ring of three
   for (int s = s_beg; s < s_end; ++s) {
-    wait_vm_lgkm0<C::YOUNGER>();   // this wave's loads of the span
+    if (s == s_beg) wait_vm_lgkm0<C::YOUNGER>();   // this wave's loads of the span
+    else wait_vm_lgkm0<C::YOUNGER + 2>();
     wg_barrier();                  // everyone's, and everyone past the span before
     const int xp = (s - s_beg) & 1;
     u32x4 x[4], codes;
@@ -309,37 +313,52 @@ __global__ __launch_bounds__(C::W * kWave) void mx_producer_shared_kernel(const 
     wait_vm_lgkm0<63>();           // x is read
     ask_x(s + 2, xp);
     ask_l(s + 2, place == 0 ? 2 : place - 1);
+    // the products' operands of step i + 1 are read before step i's products: one
+    // wave a SIMD has nothing else to hide the reads behind
+    const uint8_t* t = smem + place * C::TILE + r * 256;
+    u32x4 b[2][RT];
+    auto read_b = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < RT; ++j) b[i & 1][j] = *reinterpret_cast<const u32x4*>(t + j * 4096 + (((4 * i + g) ^ r) << 4));
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    read_b(0);
     const uint32_t byte = quantize_span<F16>(x, g, codes);
     const int k = s * 128 + 32 * g;
-    if (live && k < K) {
-      *reinterpret_cast<u32x4*>(p.act + size_t(row) * size_t(K / 2) + k / 2) = codes;
-      p.ascales[size_t(k / 32) * size_t(M) + row] = uint8_t(byte);
+    // (no branch: every wave issues both stores, which the waits count)
+    const bool keep = live && k < K;
+    __builtin_amdgcn_raw_buffer_store_b128(codes, act, keep ? act_row + uint32_t(k) / 2u : 0xFFFFFFF0u, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b8(uint8_t(byte), ascales, keep ? uint32_t(k / 32) * uint32_t(M) + uint32_t(row) : 0xFFFFFFF0u, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < 3) read_b(i + 1);
+#pragma unroll
+      for (int j = 0; j < RT; ++j) acc[j] = mfma16<F16>(x[i], b[i & 1][j], acc[j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    const uint8_t* t = smem + place * C::TILE + r * 256;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const u32x4 b = *reinterpret_cast<const u32x4*>(t + j * 4096 + (((4 * i + g) ^ r) << 4));
-        acc[j] = mfma16<F16>(x[i], b, acc[j]);
-      }
     place = place == 2 ? 0 : place + 1;
   }
   wait_vm<0>();
 
-  // lane (c, g) of tile j holds rows 4g .. 4g+3 of rank 16 j + c
+  // lane (c, g) of tile j holds rows 4g .. 4g+3 of rank 16 j + c; the descriptor
+  // drops what lies past M or R
+  const bool cut = p.ks > 1;
+  const uint32_t n = uint32_t(M) * uint32_t(R);
+  const auto sums = cut ? __builtin_amdgcn_make_buffer_rsrc(p.part + size_t(z) * n, 0, int(n * 4u), 0x00020000)
+                        : __builtin_amdgcn_make_buffer_rsrc(p.lora_act_in, 0, int(n * 2u), 0x00020000);
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
     const int rank = 16 * j + r;
-    if (rank >= R) continue;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int m = mw + 4 * g + e;
-      if (m >= M) continue;
-      if (p.ks > 1)
-        p.part[(size_t(z) * size_t(M) + m) * size_t(R) + rank] = acc[j][e];
+      const bool in = m < M && rank < R;
+      const uint32_t at = uint32_t(m) * uint32_t(R) + uint32_t(rank);
+      const float sum = acc[j][e];
+      if (cut)
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, sum), sums, in ? at * 4u : 0xFFFFFFF0u, 0, 0);
       else
-        p.lora_act_in[size_t(m) * size_t(R) + rank] = narrow<F16>(acc[j][e]);
+        __builtin_amdgcn_raw_buffer_store_b16(narrow<F16>(sum), sums, in ? at * 2u : 0xFFFFFFF0u, 0, 0);
     }
   }
 }
