@@ -46,7 +46,7 @@ struct MxProdParams {
   float* part;          // ks > 1 and R > 0: [slice][M][R] float32 sums
   int M, K, R;
   int ks, sps;          // K slices, spans per slice
-  int groups;           // workgroups that share rows and slice, a rank tile each
+  int groups;           // workgroups that share rows and slice, some rank tiles each
 };
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
@@ -247,7 +247,9 @@ __global__ __launch_bounds__(C::W * kWave) void mx_producer_shared_kernel(const 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int M = p.M, K = p.K, R = p.R;
-  const int rb = blockIdx.x / p.ks, z = blockIdx.x - rb * p.ks;
+  const int blocks = gridDim.x / p.groups;   // the groups of a block often meet on one XCD
+  const int q0 = blockIdx.x / blocks, blk = blockIdx.x - q0 * blocks;
+  const int rb = blk / p.ks, z = blk - rb * p.ks;
   const int mw = rb * C::ROWS + 16 * wave;
   const int nsp = (K + 127) / 128;
   const int s_beg = z * p.sps, s_end = min(nsp, s_beg + p.sps);
@@ -264,7 +266,7 @@ __global__ __launch_bounds__(C::W * kWave) void mx_producer_shared_kernel(const 
   }
 #pragma unroll
   for (int u = 0; u < C::LOADS; ++u) {
-    const int rank = (wave * C::LOADS + u) * 4 + g;
+    const int rank = q0 * RT * 16 + (wave * C::LOADS + u) * 4 + g;
     lk[u] = 8 * (r ^ (rank & 15));
     loff[u] = uint32_t(rank) * row_bytes + uint32_t(lk[u]) * 2u;
   }
@@ -301,7 +303,7 @@ __global__ __launch_bounds__(C::W * kWave) void mx_producer_shared_kernel(const 
   ask_l(s_beg + 1, 1);
   int place = 0;   // of the span in the ring of three
   for (int s = s_beg; s < s_end; ++s) {
-    if (s == s_beg) wait_vm_lgkm0<C::YOUNGER>();   // this wave's loads of the span
+    if (s == s_beg || q0 > 0) wait_vm_lgkm0<C::YOUNGER>();   // this wave's loads of the span
     else wait_vm_lgkm0<C::YOUNGER + 2>();
     wg_barrier();                  // everyone's, and everyone past the span before
     const int xp = (s - s_beg) & 1;
@@ -323,12 +325,14 @@ __global__ __launch_bounds__(C::W * kWave) void mx_producer_shared_kernel(const 
       __builtin_amdgcn_sched_barrier(0);
     };
     read_b(0);
-    const uint32_t byte = quantize_span<F16>(x, g, codes);
-    const int k = s * 128 + 32 * g;
-    // (no branch: every wave issues both stores, which the waits count)
-    const bool keep = live && k < K;
-    __builtin_amdgcn_raw_buffer_store_b128(codes, act, keep ? act_row + uint32_t(k) / 2u : 0xFFFFFFF0u, 0, 0);
-    __builtin_amdgcn_raw_buffer_store_b8(uint8_t(byte), ascales, keep ? uint32_t(k / 32) * uint32_t(M) + uint32_t(row) : 0xFFFFFFF0u, 0, 0);
+    if (q0 == 0) {
+      const uint32_t byte = quantize_span<F16>(x, g, codes);
+      const int k = s * 128 + 32 * g;
+      // (no branch a lane: every wave issues both stores, which the waits count)
+      const bool keep = live && k < K;
+      __builtin_amdgcn_raw_buffer_store_b128(codes, act, keep ? act_row + uint32_t(k) / 2u : 0xFFFFFFF0u, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b8(uint8_t(byte), ascales, keep ? uint32_t(k / 32) * uint32_t(M) + uint32_t(row) : 0xFFFFFFF0u, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i < 3) read_b(i + 1);
@@ -348,7 +352,7 @@ __global__ __launch_bounds__(C::W * kWave) void mx_producer_shared_kernel(const 
                         : __builtin_amdgcn_make_buffer_rsrc(p.lora_act_in, 0, int(n * 2u), 0x00020000);
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
-    const int rank = 16 * j + r;
+    const int rank = 16 * (q0 * RT + j) + r;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int m = mw + 4 * g + e;
@@ -368,9 +372,16 @@ template <bool F16>
 __global__ __launch_bounds__(256) void mx_producer_join_kernel(const MxProdParams p) {
   const size_t n = size_t(p.M) * size_t(p.R), i = size_t(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n) return;
-  float t = p.part[i];
-#pragma unroll 4
-  for (int z = 1; z < p.ks; ++z) t += p.part[size_t(z) * n + i];
+  float t = 0.f;
+  int z = 0;
+  for (; z + 8 <= p.ks; z += 8) {   // eight slices' sums in flight
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = p.part[size_t(z + u) * n + i];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) t += v[u];
+  }
+  for (; z < p.ks; ++z) t += p.part[size_t(z) * n + i];
   p.lora_act_in[i] = narrow<F16>(t);
 }
 
@@ -393,7 +404,8 @@ struct MxProdPlan {
   int threads;
   int rbs;       // row blocks
   int ks, sps;   // K slices, spans of a slice
-  int groups;    // rank tiles apart, a workgroup each
+  int tiles;     // rank tiles of a workgroup (0, 1, 2; shared: 2, 4, 8)
+  int groups;    // workgroups that share the rank tiles of rows and slice
   int64_t bytes;
 };
 
@@ -419,8 +431,20 @@ static MxProdPlan mx_prod_plan(int M, int K, int R) {
   // A workgroup for each rank tile where that leaves no compute unit with two of
   // them, and for up to 16 rows: one unit takes 2.6 us to fetch a rank tile of
   // 3072 k (4x3072 R=32: 8.3 us with both tiles in one workgroup, 6.0 apart).
-  const int tiles = (R + 15) / 16;
-  pl.groups = !pl.shared && tiles > 1 && (M <= 16 || int64_t(pl.rbs) * pl.ks * tiles <= mx_cus()) ? tiles : 1;
+  // Where lora_down is shared, pairs of tiles or more, likewise (512x3072 R=128:
+  // 8.0 us with the 8 tiles in one workgroup, 5.9 in four; 64x12288 R=128 7.7 and
+  // 5.5).
+  const int blocks = pl.rbs * pl.ks, tiles = (R + 15) / 16;
+  pl.groups = 1;
+  if (pl.shared == 4)
+    for (pl.tiles = R <= 32 ? 2 : R <= 64 ? 4 : 8; pl.tiles > 2 && int64_t(blocks) * pl.groups * 2 <= mx_cus(); pl.tiles /= 2)
+      pl.groups *= 2;
+  else if (pl.shared == 8)
+    pl.tiles = 8;
+  else {
+    if (tiles > 1 && (M <= 16 || int64_t(blocks) * tiles <= mx_cus())) pl.groups = tiles;
+    pl.tiles = pl.groups > 1 ? 1 : tiles;
+  }
   pl.bytes = pl.ks > 1 && R > 0 ? int64_t(pl.ks) * M * R * 4 : 0;
   return pl;
 }
@@ -432,15 +456,15 @@ static bool mx_prod_sizes_ok(int M, int K, int R) {
 }
 
 template <bool F16>
-static const void* mx_producer_of(int R, int shared, int groups) {
-  if (shared == 8) return reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<8, 8>>);
-  if (shared)
-    return R <= 32 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<2, 4>>)
-         : R <= 64 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<4, 4>>)
-                   : reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<8, 4>>);
-  if (R == 0) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 0>);
-  if (R <= 16 || groups > 1) return reinterpret_cast<const void*>(mx_producer_kernel<F16, 1>);
-  return reinterpret_cast<const void*>(mx_producer_kernel<F16, 2>);
+static const void* mx_producer_of(const MxProdPlan& pl) {
+  if (pl.shared == 8) return reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<8, 8>>);
+  if (pl.shared)
+    return pl.tiles == 2 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<2, 4>>)
+         : pl.tiles == 4 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<4, 4>>)
+                         : reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<8, 4>>);
+  return pl.tiles == 0 ? reinterpret_cast<const void*>(mx_producer_kernel<F16, 0>)
+       : pl.tiles == 1 ? reinterpret_cast<const void*>(mx_producer_kernel<F16, 1>)
+                       : reinterpret_cast<const void*>(mx_producer_kernel<F16, 2>);
 }
 
 template <bool F16>
@@ -473,7 +497,7 @@ static int mx_quantize_run(const uint16_t* x, const uint16_t* lora_down, uint8_t
                  M, K, R, pl.ks, pl.sps, pl.groups};
   void* args[] = {&p};
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  hipError_t e = hipLaunchKernel(mx_producer_of<F16>(R, pl.shared, pl.groups),
+  hipError_t e = hipLaunchKernel(mx_producer_of<F16>(pl),
                                  dim3(unsigned(pl.rbs) * unsigned(pl.ks) * unsigned(pl.groups)),
                                  dim3(pl.threads), args, 0, st);
   if (e == hipSuccess && pl.bytes > 0)

@@ -46,9 +46,10 @@ def test_sizes(M, K, R, dtype):
     check(activations(rng, M, K, dtype), normal_bits(rng, (R, K), dtype, 0.02) if R else None, dtype, f"{M}x{K} R{R} {dtype}")
 
 
-@pytest.mark.parametrize("M,K,R", [(3, 8224, 128), (16, 12288, 33), (12, 96, 127), (128, 4096, 32), (700, 4128, 31)])
+@pytest.mark.parametrize("M,K,R", [(3, 8224, 128), (16, 12288, 33), (12, 96, 127), (128, 4096, 32), (700, 4128, 31),
+                                   (512, 3072, 128), (100, 12288, 60), (70, 160, 128), (300, 1056, 97), (129, 8224, 128)])
 def test_rank_tiles_apart(M, K, R):
-    """Few rows: each tile of 16 ranks has a workgroup of its own, K in slices or not."""
+    """Few rows: the tiles of 16 ranks are dealt to workgroups of their own, K in slices or not."""
     print(f"case: {M} x {K} R={R}", flush=True)
     rng = np.random.default_rng(M + K + R)
     check(activations(rng, M, K, "bf16"), normal_bits(rng, (R, K), "bf16", 0.02), "bf16", f"{M}x{K} R{R}")
