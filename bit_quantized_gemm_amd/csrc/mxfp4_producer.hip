@@ -6,10 +6,10 @@
 // in the layout of the LoRA product's A operand: lane (r, g) of a wave holds row
 // r, k = 32 i + 8 g .. + 7 for the four blocks i of a 128-wide span, so that
 // four lanes read 64 neighbouring bytes (one whole block a lane, 64 bytes
-// apart, cost four times the cache cycles). 4096 x 3072, R = 32: 11.9 us, 2.7
-// TB/s (14.2 with a block a lane); past the floor it is the reading of lora_down,
-// 294 KB a compute unit, that bounds it. 1001 x 12288, R = 128: 18.9 us.
-// A block's largest magnitude meets over its four lanes by lane swaps, and so
+// apart, cost four times the cache cycles). 4096 x 3072, R = 32: 11.3 us, 2.85
+// TB/s; 1001 x 12288, R = 128: 16.0 us, 2.2 TB/s. Past the launches, each of the
+// loads, the quantisation, the products and the stores adds its part of a span's
+// chain: no one of them alone bounds it. A block's largest magnitude meets over its four lanes by lane swaps, and so
 // do its codes, which leave as 16 bytes a lane.
 //
 // The scale of a block is a power of two read off the exponent of its largest
@@ -18,10 +18,11 @@
 // scale (2^-127) included (checked against the definition over every 16-bit
 // pattern at scale bytes 0 .. 252): two values an instruction.
 //
-// The waves of a workgroup share its 16 rows and take the spans of K in turn;
-// their partial LoRA sums meet in LDS. When the row blocks do not fill the
-// chip, K is split over workgroups too; the slices' float32 sums go to the
-// caller's workspace and a second launch adds them in slice order.
+// Few ranks or rows: the waves of a workgroup share its 16 rows and take the
+// spans of K in turn; their partial LoRA sums meet in LDS. Else 16 rows a wave,
+// and lora_down shared in LDS. When the row blocks do not fill the chip, K is
+// split over workgroups too; the slices' float32 sums go to the caller's
+// workspace and a second launch adds them in slice order.
 #include <hip/hip_runtime.h>
 
 #include <stddef.h>
@@ -127,12 +128,11 @@ __device__ __forceinline__ uint32_t quantize_span(const u32x4 (&d)[4], int g, u3
 constexpr int kMxProdWaves = 8;
 
 // A workgroup a 16 rows, or one for each of `groups` rank tiles of them, of
-// which the first writes the codes. RT: rank tiles of a workgroup, 0 (no LoRA
-// product) to 2.
-template <bool F16, int RT>
+// which the first writes the codes. LORA: 0 < R.
+template <bool F16, bool LORA>
 __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const MxProdParams p) {
-  constexpr int W = kMxProdWaves, NA = RT > 0 ? RT : 1;
-  __shared__ f32x4 red[RT > 0 ? W * RT * kWave : 1];
+  constexpr int W = kMxProdWaves;
+  __shared__ f32x4 red[LORA ? W * kWave : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -144,19 +144,15 @@ __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const
   const int s_end = min(nsp, (z + 1) * p.sps);
   const int row = min(m0 + r, M - 1);   // rows past M repeat the last and are not stored
   const bool live = m0 + r < M;
+  const int rank = 16 * q0 + r;         // ranks past R repeat the last; their sums are not stored
   const uint16_t* xr = p.x + size_t(row) * size_t(K) + 8 * g;
-  const uint16_t* lr[NA];
-#pragma unroll
-  for (int j = 0; j < RT; ++j)   // ranks past R repeat the last; their sums are not stored
-    lr[j] = p.lora_down + size_t(min(16 * (q0 + j) + r, R - 1)) * size_t(K) + 8 * g;
-  f32x4 acc[NA];
-#pragma unroll
-  for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint16_t* lr = LORA ? p.lora_down + size_t(min(rank, R - 1)) * size_t(K) + 8 * g : nullptr;
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
 
   // A span's x and lora_down operands are asked for one span ahead. TAIL: the
   // span that K ends in; its blocks past K (K % 32 == 0: in or out whole) read
   // as zeros.
-  u32x4 x[2][4], b[2][4][NA];
+  u32x4 x[2][4], b[2][4];
   auto load = [&]<bool TAIL>(const uint16_t* from, int k) __attribute__((always_inline)) {
     return !TAIL || k < K ? *reinterpret_cast<const u32x4*>(from + k) : u32x4{0u, 0u, 0u, 0u};
   };
@@ -165,8 +161,7 @@ __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const
     for (int i = 0; i < 4; ++i) x[q][i] = load.template operator()<TAIL>(xr, s * 128 + 32 * i);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) b[q][i][j] = load.template operator()<TAIL>(lr[j], s * 128 + 32 * i);
+      if constexpr (LORA) b[q][i] = load.template operator()<TAIL>(lr, s * 128 + 32 * i);
   };
   auto work = [&]<bool TAIL>(int q, int s) __attribute__((always_inline)) {
     const int k = s * 128 + 32 * g;
@@ -178,8 +173,7 @@ __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[j] = mfma16<F16>(x[q][i], b[q][i][j], acc[j]);
+      if constexpr (LORA) acc = mfma16<F16>(x[q][i], b[q][i], acc);
   };
   const int e = min(s_end, K / 128);   // past the whole spans
   int s = z * p.sps + wave;
@@ -195,26 +189,23 @@ __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const
     work.template operator()<true>(0, e);
   }
 
-  if constexpr (RT > 0) {
-#pragma unroll
-    for (int j = 0; j < RT; ++j) red[(wave * RT + j) * kWave + lane] = acc[j];
+  if constexpr (LORA) {
+    red[wave * kWave + lane] = acc;
     __syncthreads();
-    // lane (c, g) of rank tile j holds rows 4g .. 4g+3 of rank 16 j + c
-    for (int j = wave; j < RT; j += W) {
-      f32x4 sum = red[j * kWave + lane];
+    if (wave != 0) return;
+    f32x4 sum = red[lane];
 #pragma unroll
-      for (int w = 1; w < W; ++w) sum += red[(w * RT + j) * kWave + lane];
-      const int rank = 16 * (q0 + j) + r;
-      if (rank >= R) continue;
+    for (int w = 1; w < W; ++w) sum += red[w * kWave + lane];
+    if (rank >= R) return;
+    // lane (c, g) holds rows 4g .. 4g+3 of rank c of the tile
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int m = m0 + 4 * g + i;
-        if (m >= M) continue;
-        if (p.ks > 1)
-          p.part[(size_t(z) * size_t(M) + m) * size_t(R) + rank] = sum[i];
-        else
-          p.lora_act_in[size_t(m) * size_t(R) + rank] = narrow<F16>(sum[i]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int m = m0 + 4 * g + i;
+      if (m >= M) continue;
+      if (p.ks > 1)
+        p.part[(size_t(z) * size_t(M) + m) * size_t(R) + rank] = sum[i];
+      else
+        p.lora_act_in[size_t(m) * size_t(R) + rank] = narrow<F16>(sum[i]);
     }
   }
 }
@@ -404,46 +395,48 @@ struct MxProdPlan {
   int threads;
   int rbs;       // row blocks
   int ks, sps;   // K slices, spans of a slice
-  int tiles;     // rank tiles of a workgroup (0, 1, 2; shared: 2, 4, 8)
+  int tiles;     // rank tiles of a workgroup (0 or 1; shared: 2, 4, 8)
   int groups;    // workgroups that share the rank tiles of rows and slice
   int64_t bytes;
 };
 
-// Which kernel, measured (binary16, us, unshared against shared of 4 waves):
-// 4096x3072 R=32 11.9 against 15.2, 4096x12288 R=32 41.6 against 29.8,
-// 16384x3072 R=32 43.2 against 26.8, 1001x12288 R=128 24.8 against 18.9: shared
-// for more than 32 ranks, and for fewer where x is large. 8 waves of shared
-// against 4: 1001x12288 R=128 19.9 and 18.9, 4096x12288 R=128 41.0 and 46.7,
-// R=64 33.5 and 31.9: for more than 64 ranks of many rows.
+// Which kernel, measured (us, with the join where there is one): unshared
+// against shared of 4 waves: 4096x3072 R=32 11.9 and 10.3, R=16 9.2 and 10.1,
+// 2048x12288 R=32 23.7 and 15.9, 256x3072 R=32 7.3 and 5.2, 3000x3072 R=8 7.7 and
+// 9.3, 256x12288 R=16 (both in slices) 8.5 and 6.8: shared for more than 16
+// ranks, and for fewer where x is large or the other would need slices too.
+// 8 waves of shared against 4: 4096x12288 R=128 38.4 and 43.5, 3000x6144 R=96
+// 18.7 and 19.8, 4096x3072 R=128 18.1 and 16.6: 8 for more than 64 ranks of a
+// large x.
 static MxProdPlan mx_prod_plan(int M, int K, int R) {
   MxProdPlan pl;
-  const bool large = M > 4096 || int64_t(M) * K >= (int64_t(1) << 25);
-  pl.shared = R > 32 ? (M <= 16 ? 0 : R > 64 && M >= 2048 ? 8 : 4) : R > 0 && large ? 4 : 0;
+  const int64_t size = int64_t(M) * K;
+  const int nsp = (K + 127) / 128;
+  const bool sliced = nsp / (2 * kMxProdWaves) > 1 && mx_cus() / ((M + 15) / 16) > 1;
+  pl.shared = M <= 16 || R == 0 ? 0
+              : R > 64 && size >= (int64_t(1) << 24) ? 8
+              : R > 16 || M > 4096 || size >= (int64_t(1) << 25) || sliced ? 4 : 0;
   const int waves = pl.shared ? pl.shared : kMxProdWaves, rows = pl.shared ? 16 * waves : 16;
   pl.threads = waves * kWave;
   pl.rbs = (M + rows - 1) / rows;
-  const int nsp = (K + 127) / 128;
   // slices that fill the chip once; of at least 2 spans a wave, or 3 of a
   // workgroup that shares them
   const int ks = std::max(1, std::min(nsp / (pl.shared ? 3 : 2 * waves), mx_cus() / pl.rbs));
   pl.sps = (nsp + ks - 1) / ks;
   pl.ks = (nsp + pl.sps - 1) / pl.sps;
-  // A workgroup for each rank tile where that leaves no compute unit with two of
-  // them, and for up to 16 rows: one unit takes 2.6 us to fetch a rank tile of
-  // 3072 k (4x3072 R=32: 8.3 us with both tiles in one workgroup, 6.0 apart).
-  // Where lora_down is shared, pairs of tiles or more, likewise (512x3072 R=128:
-  // 8.0 us with the 8 tiles in one workgroup, 5.9 in four; 64x12288 R=128 7.7 and
-  // 5.5).
-  const int blocks = pl.rbs * pl.ks, tiles = (R + 15) / 16;
-  pl.groups = 1;
-  if (pl.shared == 4)
-    for (pl.tiles = R <= 32 ? 2 : R <= 64 ? 4 : 8; pl.tiles > 2 && int64_t(blocks) * pl.groups * 2 <= mx_cus(); pl.tiles /= 2)
-      pl.groups *= 2;
-  else if (pl.shared == 8)
-    pl.tiles = 8;
-  else {
-    if (tiles > 1 && (M <= 16 || int64_t(blocks) * tiles <= mx_cus())) pl.groups = tiles;
-    pl.tiles = pl.groups > 1 ? 1 : tiles;
+  // Up to 16 rows: a workgroup for each rank tile, since one compute unit takes
+  // 2.6 us to fetch a tile of 3072 k (4x3072 R=32: 8.3 us with both tiles in one
+  // workgroup, 6.0 apart). Where lora_down is shared, pairs of tiles or more are
+  // dealt to the compute units that are free (512x3072 R=128: 8.0 us with the 8
+  // tiles in one workgroup, 5.9 in four; 64x12288 R=128 7.7 and 5.5).
+  if (pl.shared) {
+    pl.groups = 1;
+    pl.tiles = pl.shared == 8 || R > 64 ? 8 : R > 32 ? 4 : 2;
+    if (pl.shared == 4)
+      for (; pl.tiles > 2 && int64_t(pl.rbs) * pl.ks * pl.groups * 2 <= mx_cus(); pl.tiles /= 2) pl.groups *= 2;
+  } else {
+    pl.groups = std::max(1, (R + 15) / 16);
+    pl.tiles = R > 0;
   }
   pl.bytes = pl.ks > 1 && R > 0 ? int64_t(pl.ks) * M * R * 4 : 0;
   return pl;
@@ -462,9 +455,8 @@ static const void* mx_producer_of(const MxProdPlan& pl) {
     return pl.tiles == 2 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<2, 4>>)
          : pl.tiles == 4 ? reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<4, 4>>)
                          : reinterpret_cast<const void*>(mx_producer_shared_kernel<F16, MxShared<8, 4>>);
-  return pl.tiles == 0 ? reinterpret_cast<const void*>(mx_producer_kernel<F16, 0>)
-       : pl.tiles == 1 ? reinterpret_cast<const void*>(mx_producer_kernel<F16, 1>)
-                       : reinterpret_cast<const void*>(mx_producer_kernel<F16, 2>);
+  return pl.tiles ? reinterpret_cast<const void*>(mx_producer_kernel<F16, true>)
+                  : reinterpret_cast<const void*>(mx_producer_kernel<F16, false>);
 }
 
 template <bool F16>

@@ -41,7 +41,7 @@ def test_quantize_accepts():
 
 
 def test_quantize_workspace():
-    assert w4.quantize_mxfp4_workspace(4096, 3072, 32) == 0          # rows fill the chip
+    assert w4.quantize_mxfp4_workspace(4096, 3072, 16) == 0          # rows fill the chip
     assert w4.quantize_mxfp4_workspace(16, 12288, 0) == 0            # no sums to join
     assert w4.quantize_mxfp4_workspace(16, 12288, 32) > 0
     for bad in ((0, 32, 0), (1, 48, 0), (1, 32, 129)):
