@@ -5,14 +5,16 @@
 //
 // Bound by the weight bytes, N (K/2 + K/32): every weight is read once, from
 // HBM straight into the registers that the matrix instruction takes, since no
-// two waves share one. A workgroup owns 16 or 32 columns; its waves split K in
+// two waves share one. A workgroup owns 16 to 64 columns; its waves split K in
 // steps of 128 and add their sums through LDS. v_mfma_scale_f32_16x16x128_f8f6f4
 // with FP4 operands: lane (c, g) holds row c, k = 32 g .. 32 g + 31 as 16 bytes
 // and that block's scale byte. The weights are its A operand (rows n) and the
 // activations, which stay in cache, its B operand (columns m), so that a lane
 // ends with 4 neighbouring columns n of one row m. Each wave adds its share
 // of the LoRA ranks to its own sums, after the factor wcscale that the LoRA
-// term does not take.
+// term does not take. 1x12288x12288: 15.0 us, 5.3 TB/s; 1x3072x12288 7.0 and
+// 16x12288x3072 10.1, of which the launch takes 2.8. Past 16 rows the activations
+// that every workgroup reads from L2 bound it (64x12288x12288: 33 us).
 #include <hip/hip_runtime.h>
 
 #include <stddef.h>
@@ -39,6 +41,7 @@ __device__ __forceinline__ f32x4 mfma_fp4_16(u32x4 a, u32x4 b, f32x4 c, uint32_t
 template <int MT_, int NT_, int W_, int P_>
 struct FewCfg {
   static constexpr int MT = MT_, NT = NT_, W = W_, P = P_, THREADS = W * kWave, COLS = 16 * NT;
+  static constexpr bool AHEAD = MT > 1;
 };
 
 template <bool F16, class C>
@@ -49,7 +52,11 @@ __global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int M = p.M, N = p.N, K = p.K, R = p.R;
-  const int n0 = blockIdx.x * C::COLS;
+  // Workgroup b runs on XCD b % 8; each XCD takes neighbouring columns, which share
+  // the cache lines of the scales (16 columns read 16 bytes of a row of wscales:
+  // 1x12288x12288 19.0 us in order, 15.0 so).
+  const int xcd = blockIdx.x % 8, per = gridDim.x / 8, rem = gridDim.x % 8;
+  const int n0 = (xcd * per + min(xcd, rem) + int(blockIdx.x / 8)) * C::COLS;
   const int kb_all = K >> 5;
   const uint32_t rowbytes = uint32_t(K) >> 1;
   // rows and columns past the edge repeat the last and are not stored
@@ -76,36 +83,60 @@ __global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p) {
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // TAIL: the run that K ends in
-  auto run = [&]<bool TAIL>(int s0) __attribute__((always_inline)) {
-    u32x4 wv[P][NT], av[P][MT];
-    uint32_t wsv[P][NT], asv[P][MT];
+  // TAIL: the run that K ends in. More than 16 rows ask for a run's operands one
+  // run ahead (64x12288x12288 40.2 to 33.4 us); fewer have more workgroups a
+  // compute unit instead, which the registers of a run ahead would halve
+  // (1x3072x12288 7.0 to 8.6).
+  constexpr int D = C::AHEAD ? 2 : 1;
+  u32x4 wv[D][P][NT], av[D][P][MT];
+  uint32_t wsv[D][P][NT], asv[D][P][MT];
+  auto ask = [&]<bool TAIL>(int q, int s0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int s = s0 + i, kb = 4 * s + g;
       const bool in = !TAIL || kb < kb_all;   // blocks past K are zeros of scale one
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        wv[i][j] = in ? *reinterpret_cast<const u32x4*>(w[j] + 64 * s) : u32x4{0u, 0u, 0u, 0u};
-        wsv[i][j] = in ? ws[j][uint32_t(kb) * uint32_t(N)] : 127u;
+        wv[q][i][j] = in ? *reinterpret_cast<const u32x4*>(w[j] + 64 * s) : u32x4{0u, 0u, 0u, 0u};
+        wsv[q][i][j] = in ? ws[j][uint32_t(kb) * uint32_t(N)] : 127u;
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        av[i][t] = in ? *reinterpret_cast<const u32x4*>(a[t] + 64 * s) : u32x4{0u, 0u, 0u, 0u};
-        asv[i][t] = in ? as[t][uint32_t(kb) * uint32_t(M)] : 127u;
+        av[q][i][t] = in ? *reinterpret_cast<const u32x4*>(a[t] + 64 * s) : u32x4{0u, 0u, 0u, 0u};
+        asv[q][i][t] = in ? as[t][uint32_t(kb) * uint32_t(M)] : 127u;
       }
     }
+  };
+  auto products = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[j][t] = mfma_fp4_16(wv[i][j], av[i][t], acc[j][t], wsv[i][j], asv[i][t]);
+        for (int t = 0; t < MT; ++t) acc[j][t] = mfma_fp4_16(wv[q][i][j], av[q][i][t], acc[j][t], wsv[q][i][j], asv[q][i][t]);
   };
   const int full = (K >> 7) / P;   // whole runs
+  if constexpr (C::AHEAD) {
+    int s = wave;
+    if (s < full) ask.template operator()<false>(0, P * s);
 #pragma unroll 1
-  for (int s = wave; s < full; s += W) run.template operator()<false>(P * s);
-  if (K % (128 * P) != 0 && full % W == wave) run.template operator()<true>(P * full);
+    for (; s < full; s += 2 * W) {
+      if (s + W < full) ask.template operator()<false>(1, P * (s + W));
+      products(0);
+      if (s + 2 * W < full) ask.template operator()<false>(0, P * (s + 2 * W));
+      if (s + W < full) products(1);
+    }
+  } else {
+#pragma unroll 1
+    for (int s = wave; s < full; s += W) {
+      ask.template operator()<false>(0, P * s);
+      products(0);
+    }
+  }
+  if (K % (128 * P) != 0 && full % W == wave) {
+    ask.template operator()<true>(0, P * full);
+    products(0);
+  }
   // lane (c, g) of tile (j, t): columns n0 + 16 j + 4 g + e of row 16 t + c
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
@@ -202,15 +233,22 @@ static int mx_few_run(const uint8_t* act, const uint8_t* ascales, const uint8_t*
   p.K = K;
   p.R = R;
   void* args[] = {&p};
-  // Tiling, measured (us): 32 columns a workgroup, which halve the passes over
-  // the activations, where they still fill the chip (64x12288x12288 42.3
-  // against 49.8 with 16; 64x3072x12288 25.8 against 22.8); 16 waves for most
-  // rows and 16 columns (64x3072x12288 19.4 against 22.8); runs of 2 steps for
-  // few rows (1x12288x12288 19.1 against 20.3).
-  const bool wide = N >= 32 * kNumCUs;
+  // Tiling, measured (us). More than 16 rows: as many columns a workgroup as
+  // leave no compute unit without one, since each reads all activations: 32
+  // for more than 4096 columns (24x3072x6144 7.4 against 8.4 with 16,
+  // 64x3072x6144 10.3 and 15.5; 40x4096x4096 10.0 and 8.4), 64 for more than 8192
+  // (64x12288x12288 40.2 against 45.8, 30x12288x12288 25.1 and 30.6); 16 waves for most rows and 16
+  // columns (64x12288x3072 19.4 against 22.4 with 8). Up to 16 rows many
+  // workgroups a compute unit count for more: 16 columns (1x12288x12288 15.0
+  // against 18.5 with 32), runs of 2 steps (19.1 against 20.3).
+  const bool wide = N > 16 * kNumCUs, widest = N > 32 * kNumCUs;
   const FewKernel k = M <= 16 ? few_kernel<F16, FewCfg<1, 1, 8, 2>>()
-                    : M <= 32 ? (wide ? few_kernel<F16, FewCfg<2, 2, 8, 1>>() : few_kernel<F16, FewCfg<2, 1, 8, 1>>())
-                              : (wide ? few_kernel<F16, FewCfg<4, 2, 8, 1>>() : few_kernel<F16, FewCfg<4, 1, 16, 1>>());
+                    : M <= 32 ? (widest ? few_kernel<F16, FewCfg<2, 4, 8, 1>>()
+                                 : wide ? few_kernel<F16, FewCfg<2, 2, 8, 1>>()
+                                        : few_kernel<F16, FewCfg<2, 1, 8, 1>>())
+                    : widest  ? few_kernel<F16, FewCfg<4, 4, 8, 1>>()
+                    : wide    ? few_kernel<F16, FewCfg<4, 2, 8, 1>>()
+                              : few_kernel<F16, FewCfg<4, 1, 16, 1>>();
   const hipError_t e = hipLaunchKernel(k.fn, dim3((N + k.cols - 1) / k.cols), dim3(k.threads), args, 0,
                                        static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GEMM_W4A4_OK : GEMM_W4A4_ELAUNCH;

@@ -35,6 +35,16 @@ def test_sizes(M, N, K, R, dtype):
     assert_parity(bits(run(x)), y, T, f"{M}x{N}x{K} R{R} {dtype}", dtype)
 
 
+@pytest.mark.parametrize("M,N,K,R", [(1, 4112, 288, 5), (20, 4113, 2080, 33), (32, 8200, 416, 0), (33, 4100, 1056, 40),
+                                     (64, 8193, 2208, 17), (50, 8300, 96, 8), (64, 4097, 3104, 0)])
+def test_many_columns(M, N, K, R):
+    """Column counts where a workgroup takes more columns, runs of every number a wave."""
+    print(f"case: {M}x{N}x{K} R={R}", flush=True)
+    x = synthetic.custom_inputs(M, N, K, R, seed=M + N + K + R, fmt="mxfp4")
+    y, T = full_reference(x, "mxfp4")
+    assert_parity(bits(run(x)), y, T, f"{M}x{N}x{K} R{R}", "bf16")
+
+
 def test_nan_scales_and_zero_scales():
     x = synthetic.custom_inputs(5, 40, 416, 16, seed=11, fmt="mxfp4")
     x["ascales"][2, 3] = 255
