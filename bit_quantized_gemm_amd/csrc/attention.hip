@@ -78,8 +78,10 @@ __device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
 // Cutting sequences of uneven length into parts of even length: with T units of
 // kUnit keys in a sequence and `per_seq` tiles of each, parts are Q units, the
 // fewest with which all parts fit `parts` * `cut` workgroups, and a tile of the
-// sequence has ceil(T / Q) of them. Parts are numbered by sequence, tile and
-// place. Every lane of a wave looks at its own sequences (there are fewer than
+// sequence has ceil(T / Q) of them. Their places in the workspace go by sequence,
+// tile and part; workgroups take a sequence's tiles before its next part, so that
+// the heads of the same keys, neighbours in memory, are read together (8 sequences
+// of 0 to 8191 keys of 8 heads 31.8 to 31.4 us, 4 of 24 heads 45.5 to 44.5). Every lane of a wave looks at its own sequences (there are fewer than
 // 256: every one has a tile, and tiles that fill a round are not cut).
 constexpr int kUnit = 128;
 struct EvenParts {
@@ -131,8 +133,8 @@ __device__ __forceinline__ Share share_of(const AttnParams& p) {
     const EvenParts e = even_parts(p, idx, -1);
     w.idle = e.b < 0;
     if (w.idle) return w;
-    const int nth = (idx - e.start) / e.count, part = (idx - e.start) - nth * e.count;
-    w.slot = idx;
+    const int part = (idx - e.start) / p.per_seq, nth = (idx - e.start) - part * p.per_seq;
+    w.slot = e.start + nth * e.count + part;
     w.b = e.b;
     w.kvh = nth % p.kv_heads;
     w.tile = nth / p.kv_heads;
