@@ -5,15 +5,15 @@
 //
 // Bound by the weight bytes, N (K/2 + K/32): every weight is read once, from
 // HBM straight into the registers that the matrix instruction takes, since no
-// two waves share one. A workgroup owns 16 to 64 columns; its waves split K in
+// two waves share one. A workgroup owns 4 to 64 columns; its waves split K in
 // steps of 128 and add their sums through LDS. v_mfma_scale_f32_16x16x128_f8f6f4
 // with FP4 operands: lane (c, g) holds row c, k = 32 g .. 32 g + 31 as 16 bytes
 // and that block's scale byte. The weights are its A operand (rows n) and the
 // activations, which stay in cache, its B operand (columns m), so that a lane
 // ends with 4 neighbouring columns n of one row m. Each wave adds its share
 // of the LoRA ranks to its own sums, after the factor wcscale that the LoRA
-// term does not take. 1x12288x12288: 15.0 us, 5.3 TB/s; 1x3072x12288 7.0 and
-// 16x12288x3072 10.1, of which the launch takes 2.8. Past 16 rows the activations
+// term does not take. M x K x N 1x12288x12288: 15.0 us, 5.3 TB/s; 1x3072x12288 7.0 and
+// 16x12288x3072 9.4, of which the launch takes 2.8. Past 16 rows the activations
 // that every workgroup reads from L2 bound it (64x12288x12288: 33 us).
 #include <hip/hip_runtime.h>
 
@@ -45,7 +45,7 @@ struct FewCfg {
 };
 
 template <bool F16, class C>
-__global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p) {
+__global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p, int cols) {
   constexpr int W = C::W, MT = C::MT, NT = C::NT, P = C::P;
   __shared__ f32x4 red[W * NT * MT * kWave];
   const int lane = threadIdx.x & 63;
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p) {
   // the cache lines of the scales (16 columns read 16 bytes of a row of wscales:
   // 1x12288x12288 19.0 us in order, 15.0 so).
   const int xcd = blockIdx.x % 8, per = gridDim.x / 8, rem = gridDim.x % 8;
-  const int n0 = (xcd * per + min(xcd, rem) + int(blockIdx.x / 8)) * C::COLS;
+  const int n0 = (xcd * per + min(xcd, rem) + int(blockIdx.x / 8)) * cols;
   const int kb_all = K >> 5;
   const uint32_t rowbytes = uint32_t(K) >> 1;
   // rows and columns past the edge repeat the last and are not stored
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p) {
   const uint8_t* ws[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    n[j] = min(n0 + 16 * j + c, N - 1);
+    n[j] = min(n0 + min(16 * j + c, cols - 1), N - 1);
     w[j] = p.wgt + uint32_t(n[j]) * rowbytes + 16 * g;
     ws[j] = p.wscales + n[j];
   }
@@ -177,6 +177,7 @@ __global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p) {
 #pragma unroll
     for (int t = 0; t < MT; ++t) red[(wave * NT * MT + j * MT + t) * kWave + lane] = acc[j][t];
   __syncthreads();
+  const int end = min(n0 + cols, N);
   for (int u = wave; u < NT * MT; u += W) {
     f32x4 y = red[u * kWave + lane];
 #pragma unroll
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int col = n0 + 16 * (u / MT) + 4 * g + e;
-      if (col < N) p.out[uint32_t(m) * uint32_t(N) + uint32_t(col)] = narrow<F16>(y[e] + p.bias[col]);
+      if (col < end) p.out[uint32_t(m) * uint32_t(N) + uint32_t(col)] = narrow<F16>(y[e] + p.bias[col]);
     }
   }
 }
@@ -232,15 +233,14 @@ static int mx_few_run(const uint8_t* act, const uint8_t* ascales, const uint8_t*
   p.N = N;
   p.K = K;
   p.R = R;
-  void* args[] = {&p};
-  // Tiling, measured (us). More than 16 rows: as many columns a workgroup as
-  // leave no compute unit without one, since each reads all activations: 32
-  // for more than 4096 columns (24x3072x6144 7.4 against 8.4 with 16,
-  // 64x3072x6144 10.3 and 15.5; 40x4096x4096 10.0 and 8.4), 64 for more than 8192
-  // (64x12288x12288 40.2 against 45.8, 30x12288x12288 25.1 and 30.6); 16 waves for most rows and 16
-  // columns (64x12288x3072 19.4 against 22.4 with 8). Up to 16 rows many
-  // workgroups a compute unit count for more: 16 columns (1x12288x12288 15.0
-  // against 18.5 with 32), runs of 2 steps (19.1 against 20.3).
+  // Tiling, measured (M x K x N, us). More than 16 rows: as many columns a
+  // workgroup as leave no compute unit without one, since each reads all
+  // activations: 32 for more than 4096 columns (24x3072x6144 7.4 against 8.4 with
+  // 16, 64x3072x6144 10.3 and 15.5; 40x4096x4096 10.0 and 8.4), 64 for more than
+  // 8192 (64x12288x12288 40.2 against 45.8, 30x12288x12288 25.1 and 30.6); 16
+  // waves for most rows and 16 columns (64x12288x3072 19.4 against 22.4 with 8).
+  // Up to 16 rows many workgroups a compute unit count for more: 16 columns
+  // (1x12288x12288 15.0 against 18.5 with 32), runs of 2 steps (19.1 against 20.3).
   const bool wide = N > 16 * kNumCUs, widest = N > 32 * kNumCUs;
   const FewKernel k = M <= 16 ? few_kernel<F16, FewCfg<1, 1, 8, 2>>()
                     : M <= 32 ? (widest ? few_kernel<F16, FewCfg<2, 4, 8, 1>>()
@@ -249,7 +249,13 @@ static int mx_few_run(const uint8_t* act, const uint8_t* ascales, const uint8_t*
                     : widest  ? few_kernel<F16, FewCfg<4, 4, 8, 1>>()
                     : wide    ? few_kernel<F16, FewCfg<4, 2, 8, 1>>()
                               : few_kernel<F16, FewCfg<4, 1, 16, 1>>();
-  const hipError_t e = hipLaunchKernel(k.fn, dim3((N + k.cols - 1) / k.cols), dim3(k.threads), args, 0,
+  // Up to 32 rows and 16 columns a workgroup: fewer columns where that puts every
+  // compute unit to work (16x12288x3072 12 columns 9.4 against 10.2 us,
+  // 32x12288x1536 6 columns 11.1 against 12.3, 1x12288x1001 4 columns 5.0 against 6.3;
+  // 40x3072x2500 7.1 against 6.2, the activations being read more often).
+  const int cols = k.cols > 16 || M > 32 ? k.cols : std::min(16, std::max(4, (N + kNumCUs - 1) / kNumCUs));
+  void* args[] = {&p, const_cast<int*>(&cols)};
+  const hipError_t e = hipLaunchKernel(k.fn, dim3((N + cols - 1) / cols), dim3(k.threads), args, 0,
                                        static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GEMM_W4A4_OK : GEMM_W4A4_ELAUNCH;
 }

@@ -36,9 +36,10 @@ def test_sizes(M, N, K, R, dtype):
 
 
 @pytest.mark.parametrize("M,N,K,R", [(1, 4112, 288, 5), (20, 4113, 2080, 33), (32, 8200, 416, 0), (33, 4100, 1056, 40),
-                                     (64, 8193, 2208, 17), (50, 8300, 96, 8), (64, 4097, 3104, 0)])
-def test_many_columns(M, N, K, R):
-    """Column counts where a workgroup takes more columns, runs of every number a wave."""
+                                     (64, 8193, 2208, 17), (50, 8300, 96, 8), (64, 4097, 3104, 0),
+                                     (9, 1023, 608, 9), (30, 1025, 1056, 32), (3, 2817, 12288, 20), (17, 3841, 160, 1)])
+def test_columns_of_a_workgroup(M, N, K, R):
+    """Column counts around which a workgroup takes more or fewer columns, a wave more or fewer runs."""
     print(f"case: {M}x{N}x{K} R={R}", flush=True)
     x = synthetic.custom_inputs(M, N, K, R, seed=M + N + K + R, fmt="mxfp4")
     y, T = full_reference(x, "mxfp4")
