@@ -215,7 +215,9 @@ __global__ __launch_bounds__(kMxProdWaves * kWave) void mx_producer_kernel(const
 // wave, and its waves share each span's lora_down tile in LDS. Both it and the
 // waves' own x come by direct-to-LDS loads two spans ahead, lora_down in a ring
 // of three, x in one of two (a wave has read its x before it asks for more).
-// The chunks of a row are XOR-swizzled by row: no read meets a bank twice.
+// The chunks of a row are XOR-swizzled by row: no read meets a bank twice. 32
+// rows a wave would halve the reads of lora_down from LDS, but its fewer waves
+// cost more (4096 x 12288, R = 128: 40.4 us against 35.5).
 template <int RT_, int W_>
 struct MxShared {
   static constexpr int RT = RT_, W = W_, ROWS = 16 * W, RING = 3;
