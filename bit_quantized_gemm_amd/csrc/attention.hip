@@ -447,7 +447,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
 //
 // Rings of four 32-key tiles of K and of V, loaded two steps before they are
 // read, one meeting of the workgroup a step. 4352 x 4608 keys, 24 heads of 128:
-// 247 us, 997 TFLOP/s of the 1228 that a large product reaches here; the matrix
+// 246 to 256 us, 963 to 1003 TFLOP/s of the 1228 that a large product reaches here; the matrix
 // cores, the exponentials and the LDS reads share the issue slots. 4096 x 512
 // keys: 34 us, 750 TFLOP/s, with 768 tiles for 512 places.
 //
