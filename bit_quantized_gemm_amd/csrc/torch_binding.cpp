@@ -243,26 +243,29 @@ PyObject* rotary(PyObject* const* a) {
   const Tensor& pos = tensor(a[1], "positions");
   const Tensor& freq = tensor(a[2], "inv_freq");
   rotary_axes_t r{};
+  PyObject* seq = PySequence_Fast(a[3], "sections must be a sequence");
+  if (!seq) throw Raised{};
+  const Py_ssize_t axes = PySequence_Fast_GET_SIZE(seq);
+  int64_t pairs = 0;
+  bool fit = true;   // every section in 0 .. INT32_MAX
+  for (Py_ssize_t i = 0; i < axes && i < ROTARY_AXES_MAX && fit; ++i) {
+    int past = 0;    // sign of what long does not hold
+    const long n = PyLong_AsLongAndOverflow(PySequence_Fast_GET_ITEM(seq, i), &past);
+    fit = past == 0 && n >= 0 && n <= INT32_MAX;
+    r.sections[i] = fit ? int(n) : 0;
+    pairs += r.sections[i];
+  }
+  Py_DECREF(seq);
+  if (PyErr_Occurred()) throw Raised{};
+  if (axes < 1 || axes > ROTARY_AXES_MAX)
+    raise(PyExc_ValueError, "1 to " + std::to_string(ROTARY_AXES_MAX) + " axes, got " + std::to_string(axes));
+  if (!fit) raise(PyExc_ValueError, "sections must be 0 or more pairs each, below 2^31");
   r.f16 = half_of(x, "x");
   if (x.dim() != 4) raise(PyExc_ValueError, "x must be [batch, tokens, heads, head_dim]");
   r.batch = dim_of(x.size(0), "x");
   r.tokens = dim_of(x.size(1), "x");
   r.heads = dim_of(x.size(2), "x");
   r.head_dim = dim_of(x.size(3), "x");
-  PyObject* seq = PySequence_Fast(a[3], "sections must be a sequence");
-  if (!seq) throw Raised{};
-  const Py_ssize_t axes = PySequence_Fast_GET_SIZE(seq);
-  int64_t pairs = 0;
-  for (Py_ssize_t i = 0; i < axes && i < ROTARY_AXES_MAX; ++i) {
-    const long n = PyLong_AsLong(PySequence_Fast_GET_ITEM(seq, i));
-    if (n < -1 || n > INT32_MAX || (n == -1 && PyErr_Occurred())) break;
-    r.sections[i] = int(n);
-    pairs += n;
-  }
-  Py_DECREF(seq);
-  if (PyErr_Occurred()) throw Raised{};
-  if (axes < 1 || axes > ROTARY_AXES_MAX)
-    raise(PyExc_ValueError, "1 to " + std::to_string(ROTARY_AXES_MAX) + " axes, got " + std::to_string(axes));
   r.axes = int(axes);
   if (pos.scalar_type() != at::kInt || freq.scalar_type() != at::kFloat)
     raise(PyExc_TypeError, "positions must be int32 and inv_freq float32");
