@@ -194,7 +194,9 @@ def _run(name, stream, *args):
     else:
         import torch
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=args[0].device)
+            # 0 is the default stream, which ExternalStream would take for "one of the pool"
+            device, handle = args[0].device, int(stream)
+            stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
         with torch.cuda.stream(stream):
             r = fn(*args)
     if type(r) is int:
