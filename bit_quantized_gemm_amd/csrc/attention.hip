@@ -203,6 +203,18 @@ __device__ __forceinline__ float other_sum(float v) {
   return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
 }
 
+// A weight is exp2(s c - m), s c in one fma with the rounded maximum m, so that
+// the top score's own is 2^r, r the rounding of its product: at most 1 up to this
+// magnitude of m, and scores whose weights no longer fit a float32 (r = 128), or 16
+// bits (r = 16), 2^8 or 2^4 times past it. Beyond it s c is rounded before m is taken
+// away: the maximum's weight is 1, as it is in float32 scores.
+constexpr float kFar = 16777216.f;
+// (kept from being contracted into what it is subtracted from)
+__device__ __forceinline__ float rounded_product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+
 // A row's result from its sums o (values 8 (i / 4) + 4 h + i % 4 of each 32),
 // maximum m and sum l, or its part of them. r: the row in its tile.
 template <bool F16, class C>
@@ -353,11 +365,18 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
         for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
     }
     m = mn;
+    float cs = p.c;
+    if (__builtin_amdgcn_ballot_w64(fabsf(ms) > kFar)) {
+      const bool far = fabsf(ms) > kFar;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sc[i] = far ? rounded_product(sc[i], p.c) : sc[i];
+      cs = far ? 1.f : cs;
+    }
     u32x4 pv[2];
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
-      const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], p.c, -ms));
-      const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i + 1], p.c, -ms));
+      const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], cs, -ms));
+      const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i + 1], cs, -ms));
       l += e0 + e1;
       pv[i >> 3][(i >> 1) & 3] = narrow2<F16>(e0, e1);
     }
@@ -556,7 +575,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
   // The softmax of a step in parts: the maximum by quarters and what follows
   // from it, then the weights one key at a time.
   constexpr int FIN = 8, PARTS = FIN + 16;
-  float alpha, ms, top, grown, drop, e[4];
+  float alpha, ms, top, grown, drop, lold, e[4];
   auto soft = [&]<bool TAIL>(int part, f32x16& s, u32x4 (&wt)[2], int key0) __attribute__((always_inline)) {
     if (part < 4) {
       if constexpr (TAIL) {
@@ -574,7 +593,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
       // the maximum in use grows, or stays and alpha, the factor of what was
       // summed before, is 1 (the first keys: m is -inf)
       top *= p.c;
-      grown = top > m + kSlack ? top : m;
+      grown = top - m > kSlack ? top : m;
     } else if (part == 6) {
       drop = m == grown ? 0.f : m - grown;
       ms = grown == -INFINITY ? 0.f : grown;
@@ -582,6 +601,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
     } else if (part == 7) {
       alpha = __builtin_amdgcn_exp2f(drop);
       l *= alpha;
+      lold = l;
     } else {
       // an exponential is used one part after it was asked for
       const int i = part - FIN;
@@ -638,11 +658,21 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
     __builtin_amdgcn_sched_barrier(0);
     // (the compiler would move the weights past the branch, away from the MFMAs)
     asm volatile("" : "+v"(pv[P][0]), "+v"(pv[P][1]), "+v"(l));
-    if (__builtin_amdgcn_ballot_w64(alpha != 1.f)) {
+    if (__builtin_amdgcn_ballot_w64(alpha != 1.f || fabsf(ms) > kFar)) {
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+      if (fabsf(ms) > kFar) {   // these rows' weights and sum again, scores rounded first
+        l = lold;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float e0 = __builtin_amdgcn_exp2f(rounded_product(sc[P][i], p.c) - ms);
+          const float e1 = __builtin_amdgcn_exp2f(rounded_product(sc[P][i + 1], p.c) - ms);
+          l += e0 + e1;
+          pv[P][i >> 3][(i >> 1) & 3] = narrow2<F16>(e0, e1);
+        }
+      }
     }
   };
   static_assert(C::RING == 4 && MFMAS >= 8, "the step above");
