@@ -138,20 +138,31 @@ __global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p, int 
     products(0);
   }
   // lane (c, g) of tile (j, t): columns n0 + 16 j + 4 g + e of row 16 t + c
+  float wc[NT][4];
+  bool large = false;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    float wc[4];
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) wc[e] = p.wcscale[min(n0 + 16 * j + 4 * g + e, N - 1)];
+    for (int e = 0; e < 4; ++e) {
+      wc[j][e] = p.wcscale[min(n0 + 16 * j + 4 * g + e, N - 1)];
+      large |= !(fabsf(wc[j][e]) < 0x1p64f);
+    }
+  // A factor that is infinite, NaN or so large that a wave's part of a finite sum could
+  // become infinite (parts of both signs, or none, would then add up to NaN): the
+  // waves' sums meet without it and without the LoRA term. The same in every wave.
+  const bool apart = __builtin_amdgcn_ballot_w64(large) != 0;
+  if (!apart) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][t][e] *= wc[e];
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][t][e] *= wc[j][e];
   }
 
   // ranks r0 .. r0+31: lane (c, g) supplies ranks r0 + 8g .. +7 of column n
   // (A) and of row m (B)
-  for (int r0 = 32 * wave; r0 < R; r0 += 32 * W) {
+  for (int r0 = 32 * wave; r0 < (apart ? 0 : R); r0 += 32 * W) {
     const int rr = r0 + 8 * g;
     u32x4 uv[NT];
 #pragma unroll
@@ -187,7 +198,14 @@ __global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p, int 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int col = n0 + 16 * (u / MT) + 4 * g + e;
-      if (col < end) p.out[uint32_t(m) * uint32_t(N) + uint32_t(col)] = narrow<F16>(y[e] + p.bias[col]);
+      if (col >= end) continue;
+      float v = y[e];
+      if (apart) {
+        v *= p.wcscale[col];
+        for (int r = 0; r < R; ++r)
+          v += widen<F16>(p.lora_act_in[uint32_t(m) * uint32_t(R) + uint32_t(r)]) * widen<F16>(p.lora_up[uint32_t(r) * uint32_t(N) + uint32_t(col)]);
+      }
+      p.out[uint32_t(m) * uint32_t(N) + uint32_t(col)] = narrow<F16>(v + p.bias[col]);
     }
   }
 }
