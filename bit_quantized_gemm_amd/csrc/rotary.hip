@@ -40,23 +40,15 @@ struct RotaryParams {
   int inverse;
 };
 
-// cos and sin of pos * freq. The angle in turns, t = pos * freq / (2 pi), is
-// kept as a float32 product and the two rounding errors beside it (1/(2 pi)
-// as a float32 pair), so that its fraction is good to about 2^-23 turns
-// whatever the position; the sine and cosine instructions take turns.
+// cos and sin of pos * freq. The angle in turns is held in float64, whose rounding
+// moves it by |pos * freq| / 2 pi * 2^-52 turns at most (2^-23 for a position of 2^31
+// and a frequency of 1); its fraction, rounded to float32, by 2^-25 more. The sine
+// and cosine instructions take turns.
 __device__ __forceinline__ void turn(int pos, float freq, float& c, float& s) {
-  const float inv_hi = 0.15915494f, inv_lo = 6.4206382e-9f;   // 1/(2 pi) = hi + lo
-  const float f = freq * inv_hi;
-  const float fe = __builtin_fmaf(freq, inv_lo, __builtin_fmaf(freq, inv_hi, -f));
-  // positions past 2^24 are not float32 numbers: carry what is left over (the
-  // largest are kept from rounding up to 2^31, which int cannot hold)
-  const float p = fminf(float(pos), 2147483520.f);
-  const float pe = float(pos - int(p));
-  const float t = p * f;
-  const float te = __builtin_fmaf(p, f, -t) + p * fe + pe * f;
-  const float a = __builtin_amdgcn_fractf(t) + te;
-  c = __builtin_amdgcn_cosf(__builtin_amdgcn_fractf(a));
-  s = __builtin_amdgcn_sinf(__builtin_amdgcn_fractf(a));
+  const double t = double(pos) * (double(freq) * 0.15915494309189535);
+  const float a = float(__builtin_amdgcn_fract(t));
+  c = __builtin_amdgcn_cosf(a);
+  s = __builtin_amdgcn_sinf(a);
 }
 
 template <int V>

@@ -403,8 +403,8 @@ int gemm_mxfp4_few_f16(const uint8_t* act, const uint8_t* ascales,
  * where (u, w) are elements (2j, 2j+1) when interleaved, else (j, j + P).
  * Elements from 2P on are copied. `inverse` turns by -t: the backward pass,
  * since a rotation's transpose is the opposite rotation. The angle is reduced
- * to one turn with the product's float32 rounding error carried along, so it
- * holds for large positions; rotation in float32, rounded once.
+ * to one turn in float64, so it holds at every position (within 2^-22 turns for
+ * frequencies up to 1); rotation in float32, rounded once.
  *
  * Strides are in elements; the last dimension is dense; positions' axes are
  * dense (stride 1), with a stride per batch (0: shared) and per token. out may
