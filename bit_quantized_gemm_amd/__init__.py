@@ -184,6 +184,8 @@ def quantize_w4a4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=Non
 # ---------------------------------------------------------------- operators around the layers
 #
 # Checks, allocation and the call are one native step (csrc/torch_binding.cpp).
+# None of them records a gradient: results are detached, whatever the inputs
+# require. A tensor given as an output counts as changed in place for autograd.
 
 
 def _run(name, stream, *args):
@@ -210,14 +212,15 @@ def quantize_mxfp4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=No
     gemm_mxfp4 and gemm_mxfp4_few) and, when lora_down [R, K] of x's type is
     given, lora_act_in [M, R] = x @ lora_down^T of that type. Without lora_down
     it also lays out weights [N, K]. Outputs are allocated when None.
-    Returns (act, ascales, lora_act_in or None)."""
+    Returns (act, ascales, lora_act_in or None), detached: no gradient is recorded."""
     return _run("quantize_mxfp4_act", stream, x, lora_down, act, ascales, lora_act_in)
 
 
 def gemm_mxfp4_few(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, lora_up=None,
                    out=None, stream=None, dtype=None):
     """Enqueue the fused MXFP4 operator for few rows (M <= FEW_MAX_M): arguments
-    and result as gemm_mxfp4, in a kernel that streams the weights once.
+    and result as gemm_mxfp4, in a kernel that streams the weights once. No
+    gradient is recorded.
     """
     return _run("gemm_mxfp4_few", stream, act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out, dtype)
 
@@ -231,8 +234,9 @@ def rotary_axes(x, positions, inv_freq, sections, interleaved=True, inverse=Fals
     batch); sections: pairs per axis, dealt in order; inv_freq float32
     [sum(sections)], the angle per unit of position of each pair. Pairs are
     elements (2j, 2j+1) when interleaved, else (j, j + P), P = sum(sections);
-    elements from 2P on are copied. inverse turns the other way: the gradient
-    of x from the gradient of the result. out: allocated (dense) when None; x
+    elements from 2P on are copied. inverse turns the other way, which makes the
+    gradient of x from the gradient of the result; the call itself records no
+    gradient, so that a backward pass calls it by itself. out: allocated (dense) when None; x
     itself for in place. Returns out.
     """
     return _run("rotary_axes", stream, x, positions, inv_freq, sections, interleaved, inverse, out)
@@ -249,6 +253,6 @@ def cross_attention(q, k, v, kv_lens=None, scale=None, return_lse=False, out=Non
     each sequence (None: all); rows without keys give 0. scale: default
     head_dim ** -0.5. Returns out [batch, q_len, q_heads, head_dim] (allocated
     dense when None), and with return_lse also the float32 log-sum-exp
-    [batch, q_heads, q_len] (-inf for rows without keys).
+    [batch, q_heads, q_len] (-inf for rows without keys). No gradient is recorded.
     """
     return _run("cross_attention", stream, q, k, v, kv_lens, scale, return_lse, out)

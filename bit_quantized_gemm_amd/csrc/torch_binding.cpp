@@ -92,6 +92,14 @@ Tensor output(PyObject* o, const char* name, std::initializer_list<int64_t> shap
   return t;
 }
 
+// A tensor that the caller gave has been written: for autograd an in-place change, so
+// that a backward pass that saved it raises instead of reading the new values.
+void written(PyObject* o) {
+  if (o == Py_None) return;
+  const Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();   // (inference tensors have no version)
+}
+
 PyObject* g_stream_of = nullptr;   // torch._C._cuda_getCurrentRawStream
 
 // The device made current for the call, and its current stream.
@@ -161,6 +169,9 @@ PyObject* quantize(PyObject* const* a) {
       ptr<uint16_t>(x), static_cast<const uint16_t*>(down), ptr<uint8_t>(act), ptr<uint8_t>(scales),
       R > 0 ? ptr<uint16_t>(low) : nullptr, M, K, R, need > 0 ? ws.data_ptr() : nullptr, need, on.stream);
   if (rc != GEMM_W4A4_OK) return PyLong_FromLong(rc);
+  written(a[2]);
+  written(a[3]);
+  if (R > 0) written(a[4]);
   PyObject* r = PyTuple_New(3);
   if (!r) return nullptr;
   PyTuple_SET_ITEM(r, 0, wrap(act));
@@ -224,7 +235,9 @@ PyObject* few(PyObject* const* a) {
   const int rc = (type == at::kHalf ? gemm_mxfp4_few_f16 : gemm_mxfp4_few)(
       ptr<uint8_t>(act), ptr<uint8_t>(as), ptr<uint8_t>(wgt), ptr<uint8_t>(ws), ptr<float>(wc), ptr<float>(bias), la, lu,
       ptr<uint16_t>(out), M, N, K, R, on.stream);
-  return rc == GEMM_W4A4_OK ? wrap(out) : PyLong_FromLong(rc);
+  if (rc != GEMM_W4A4_OK) return PyLong_FromLong(rc);
+  written(a[8]);
+  return wrap(out);
 }
 
 void outer_strides(int64_t (&to)[3], const Tensor& t, const char* name) {
@@ -297,7 +310,9 @@ PyObject* rotary(PyObject* const* a) {
   r.inv_freq = ptr<float>(freq);
   const OnDevice on(x.device());
   const int rc = rotary_axes(&r, on.stream);
-  return rc == GEMM_W4A4_OK ? wrap(out) : PyLong_FromLong(rc);
+  if (rc != GEMM_W4A4_OK) return PyLong_FromLong(rc);
+  written(a[6]);
+  return wrap(out);
 }
 
 PyObject* attention(PyObject* const* a) {
@@ -354,6 +369,7 @@ PyObject* attention(PyObject* const* a) {
   }
   const int rc = cross_attention(&c, on.stream);
   if (rc != GEMM_W4A4_OK) return PyLong_FromLong(rc);
+  written(a[6]);
   if (!lse.defined()) return wrap(out);
   PyObject* r = PyTuple_New(2);
   if (!r) return nullptr;

@@ -401,8 +401,9 @@ int gemm_mxfp4_few_f16(const uint8_t* act, const uint8_t* ascales,
  *     (u, w) -> (u cos t - w sin t, u sin t + w cos t)
  *
  * where (u, w) are elements (2j, 2j+1) when interleaved, else (j, j + P).
- * Elements from 2P on are copied. `inverse` turns by -t: the backward pass,
- * since a rotation's transpose is the opposite rotation. The angle is reduced
+ * Elements from 2P on are copied. `inverse` turns by -t, which
+ * takes the gradient of out to that of x: a rotation's transpose is the opposite
+ * rotation. The angle is reduced
  * to one turn in float64, so it holds at every position (within 2^-22 turns for
  * frequencies up to 1); rotation in float32, rounded once.
  *
