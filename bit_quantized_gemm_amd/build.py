@@ -5,7 +5,9 @@
 writes bit_quantized_gemm_amd/libgemm_w4a4.so (the operator: include/gemm_w4a4.h)
 and bit_quantized_gemm_amd/libw4a4_probes.so (measurement aids:
 include/w4a4_probes.h), and bit_quantized_gemm_amd/_torch_binding.so (the native
-part of the Python binding, host code over torch's C++ interface). The kernels are compiled for gfx950 only, with
+part of the Python binding, host code over torch's C++ interface; left out, with a
+message, where torch or Python's headers are missing, so that the C library
+builds without them). The kernels are compiled for gfx950 only, with
 packed-fp32 VALU instructions disabled.
 
 Each source is compiled to an object first (in parallel). For the operator
@@ -16,11 +18,13 @@ registers of the kernel it would run from the compiled code itself.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -157,10 +161,17 @@ def _build_one(path: str, sources, with_resources: bool, verbose: bool) -> None:
     os.replace(tmp, path)
 
 
+def binding_lacks() -> str:
+    """What the torch binding cannot be built without and is missing here ("": nothing)."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return ""
+
+
 def _build_binding(verbose: bool) -> None:
     """The torch binding over the operator library (g++, host code; found beside the library at run time)."""
-    import sysconfig
-
     from torch.utils.cpp_extension import include_paths, library_paths
     tmp = BINDING_PATH + ".tmp"
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-I{INCLUDE}",
@@ -176,10 +187,15 @@ def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     for path, (sources, with_res) in LIBS.items():
         _build_one(path, sources, with_res, verbose)
-    _build_binding(verbose)
+    lacks = binding_lacks()
+    if lacks:
+        print(f"{os.path.basename(BINDING_PATH)} is not built: {lacks} is missing; the C library is complete, the "
+              "Python calls of the block operators will raise", file=sys.stderr)
+    else:
+        _build_binding(verbose)
     return LIB_PATH
 
 
 if __name__ == "__main__":
     build(verbose=True)
-    print("\n".join(list(LIBS) + [BINDING_PATH]))
+    print("\n".join(list(LIBS) + ([] if binding_lacks() else [BINDING_PATH])))
