@@ -219,8 +219,9 @@ def quantize_mxfp4_act(x, lora_down=None, act=None, ascales=None, lora_act_in=No
 def gemm_mxfp4_few(act, ascales, wgt, wscales, wcscale, bias, lora_act_in=None, lora_up=None,
                    out=None, stream=None, dtype=None):
     """Enqueue the fused MXFP4 operator for few rows (M <= FEW_MAX_M): arguments
-    and result as gemm_mxfp4, in a kernel that streams the weights once. No
-    gradient is recorded.
+    and result as gemm_mxfp4, in a kernel that streams the weights once: the
+    faster of the two, but for 16 rows or more, M % 4 == 0, and some 16384 columns.
+    No gradient is recorded.
     """
     return _run("gemm_mxfp4_few", stream, act, ascales, wgt, wscales, wcscale, bias, lora_act_in, lora_up, out, dtype)
 
@@ -229,7 +230,8 @@ def rotary_axes(x, positions, inv_freq, sections, interleaved=True, inverse=Fals
     """Enqueue rotary positions over several axes on `stream`.
 
     x bfloat16 or float16 [batch, tokens, heads, head_dim], any strides with a
-    dense last dimension (the rotated heads of a joint projection, say);
+    dense last dimension (the rotated heads of a joint projection, say), at most
+    65535 batches, head_dim up to ROTARY_MAX_HEAD_DIM;
     positions int32 [batch, tokens, axes] or [tokens, axes] (shared by the
     batch); sections: pairs per axis, dealt in order; inv_freq float32
     [sum(sections)], the angle per unit of position of each pair. Pairs are

@@ -21,6 +21,13 @@
 // 16-byte chunks are XOR-swizzled by row so that no read meets a bank twice (K:
 // reads of 16 rows at one chunk; V: transposing reads of 4 rows at four).
 //
+// That rounding is what the matrix instruction costs: it takes 16-bit operands, and
+// weights in float32 (or as two 16-bit parts) would run the second product at an
+// eighth (half) of its rate. A weight is off by half a unit of the 16-bit type, out
+// 1.2 to 1.4 times as far from 64 bits as with float32 weights (bfloat16 0.0021 to 0.0023 of its
+// size against 0.0017, f16 0.00029 against 0.00021); the sum that divides is of
+// the unrounded weights.
+//
 // Rows of a (sequence, key head) are (token, query head of the group) pairs, so
 // heads that share keys share a tile. Few rows: the waves of a workgroup take
 // different keys for the same 32 rows and join in LDS, and the keys of
@@ -466,9 +473,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
 //
 // Rings of four 32-key tiles of K and of V, loaded two steps before they are
 // read, one meeting of the workgroup a step. 4352 x 4608 keys, 24 heads of 128:
-// 246 to 256 us, 963 to 1003 TFLOP/s of the 1228 that a large product reaches here; the matrix
-// cores, the exponentials and the LDS reads share the issue slots. 4096 x 512
-// keys: 34 us, 750 TFLOP/s, with 768 tiles for 512 places.
+// 246 to 282 us from card to card, 873 to 1003 TFLOP/s of the 1228 that a large
+// product reaches; the matrix cores, the exponentials and the LDS reads share the
+// issue slots. 4096 x 512 keys: 34 to 39 us, 661 to 750 TFLOP/s, with 768 tiles for
+// 512 places.
 //
 // The sums are rescaled only when a row's maximum has grown by more than
 // kSlack (in powers of two) past the one its weights are taken against; until
@@ -629,9 +637,11 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
   };
   // Step j; R: j % RING. Reads K tile j + 1 and V tile j - 1 and, at its end,
   // the first operands of step j + 1 (K tile j + 2, V tile j). In its second
-  // half, K tile j + 3 and V tile j + 1 go to LDS, over K tile j - 1 and V tile
-  // j - 3, last read in step j - 2 (before every wave met in step j - 1); they
-  // are published by the meeting of step j + 1, and first read after it.
+  // half, after the workgroup has met, K tile j + 4 and V tile j + 2 go to LDS, over
+  // K tile j and V tile j - 2, which every wave last read in step j - 1: that meeting
+  // is all that keeps the loads behind those reads. The loads are waited for at the
+  // meeting of step j + 2 (only those of step j + 1 are younger), which publishes
+  // them; K tile j + 4 and V tile j + 2 are first read at that step's end.
   auto step = [&]<bool TAIL, int R>(int j) __attribute__((always_inline)) {
     constexpr int P = R & 1;
     static_for<0, MFMAS>([&]<int I>() __attribute__((always_inline)) {
@@ -803,7 +813,14 @@ static bool attn_sizes_ok(const cross_attention_t* a) {
 
 // Tiles and which of them are cut. Up to 32 rows (token, query head of the
 // group) a pair, or rows of v that overlap in memory (which only that kernel
-// masks): the few-row kernel; else 128-row tiles; two workgroups a compute unit. Tiles that fill no whole round of the compute
+// masks): the few-row kernel; else 128-row tiles; two workgroups a compute unit.
+// Both measured (us, 32-row tiles against 128-row ones): 32 rows, 512 pairs of 1024
+// keys 53.0 and 54.9, 128 pairs of 0 to 8191 of head size 64 41.8 and 49.8, 24 pairs
+// of 512 10.2 and 11.6; 33 rows 88.4 and 55.8, 79.9 and 51.3, 10.3 and 11.7; 128 rows
+// 164 and 63.6, 96.7 and 56.4, 12.3 and 14.8. Past 32 rows 32-row tiles read the keys
+// more than once, which costs up to three times where the tiles fill the chip and gains
+// up to 1.4 times where they do not (32 pairs of 4096 keys, 128 rows: 26.8 and 38.0).
+// Tiles that fill no whole round of the compute
 // units are cut into the parts that would fill it, of at least kMinPart keys;
 // where sequences have lengths of their own and few rows, into parts of even
 // length (8 sequences of 0 to 8191 keys, one token: 41.2 to 37.0 us).

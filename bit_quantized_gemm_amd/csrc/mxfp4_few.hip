@@ -251,9 +251,10 @@ static int mx_few_run(const uint8_t* act, const uint8_t* ascales, const uint8_t*
   p.N = N;
   p.K = K;
   p.R = R;
-  // Tiling, measured (M x K x N, us). More than 16 rows: as many columns a
-  // workgroup as leave no compute unit without one, since each reads all
-  // activations: 32 for more than 4096 columns (24x3072x6144 7.4 against 8.4 with
+  // Tiling, measured (M x K x N, us). More than 16 rows: more columns a workgroup
+  // where there are many, since each reads all activations, even though just past
+  // a threshold that leaves half of the compute units without one (N = 4097 and 8193:
+  // 129 workgroups; N = 12288 with 64 columns: 192 of 256 units): 32 for more than 4096 columns (24x3072x6144 7.4 against 8.4 with
   // 16, 64x3072x6144 10.3 and 15.5; 40x4096x4096 10.0 and 8.4), 64 for more than
   // 8192 (64x12288x12288 40.2 against 45.8, 30x12288x12288 25.1 and 30.6); 16
   // waves for most rows and 16 columns (64x12288x3072 19.4 against 22.4 with 8).
