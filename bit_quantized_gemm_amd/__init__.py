@@ -195,10 +195,14 @@ def _run(name, stream, *args):
         r = fn(*args)
     else:
         import torch
+        device = args[0].device
         if not hasattr(stream, "cuda_stream"):
             # 0 is the default stream, which ExternalStream would take for "one of the pool"
-            device, handle = args[0].device, int(stream)
+            handle = int(stream)
             stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+        elif device.type == "cuda" and stream.device != device:
+            # (the native step would take the current stream of the tensors' device)
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):
             r = fn(*args)
     if type(r) is int:
