@@ -806,8 +806,10 @@ static bool attn_sizes_ok(const cross_attention_t* a) {
   if (!a || a->batch < 0 || a->q_len < 0 || a->kv_len < 0 || a->q_heads < 0 || a->kv_heads < 1) return false;
   if (a->q_heads % a->kv_heads != 0) return false;
   if (a->head_dim < 8 || a->head_dim > CROSS_ATTENTION_MAX_HEAD_DIM || a->head_dim % 8 != 0) return false;
-  const int64_t lim = int64_t(1) << 31;
-  return int64_t(a->q_len) * a->q_heads < lim && int64_t(a->batch) * a->kv_heads < lim / 256 &&
+  // Rows and keys are counted in int, rounded up to tiles and, for loads asked for
+  // ahead, a few tiles past the end.
+  const int64_t lim = int64_t(1) << 31, most = lim - CROSS_ATTENTION_PAST_END;
+  return int64_t(a->q_len) * a->q_heads <= most && a->kv_len <= most && int64_t(a->batch) * a->kv_heads < lim / 256 &&
          int64_t(a->batch) * a->q_len * a->q_heads < lim;
 }
 

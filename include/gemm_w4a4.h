@@ -457,7 +457,9 @@ int rotary_axes(const rotary_axes_t* args, void* stream);
  * the product with v.
  *
  * scale: positive, at most 1e30. head_dim: a multiple of 8, 8 ..
- * CROSS_ATTENTION_MAX_HEAD_DIM; q_heads a multiple of kv_heads. Strides in elements, multiples of 8 (a dimension of
+ * CROSS_ATTENTION_MAX_HEAD_DIM; q_heads a multiple of kv_heads; q_len * q_heads
+ * and kv_len at most 2^31 - CROSS_ATTENTION_PAST_END, batch * q_len * q_heads below
+ * 2^31, batch * kv_heads below 2^23. Strides in elements, multiples of 8 (a dimension of
  * size 1 excepted), non-negative, k's and v's token strides below 2^23; the
  * last dimension is dense; all four tensors 16-byte aligned. q, k and v may
  * repeat memory (stride 0); out may not (GEMM_W4A4_EINVAL) and out and lse may
@@ -471,6 +473,7 @@ int rotary_axes(const rotary_axes_t* args, void* stream);
  * fixed order. Deterministic; no allocation, no synchronisation.
  */
 #define CROSS_ATTENTION_MAX_HEAD_DIM 128
+#define CROSS_ATTENTION_PAST_END 1024
 typedef struct {
   const void* q;
   const void* k;
