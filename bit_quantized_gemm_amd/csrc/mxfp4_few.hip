@@ -195,17 +195,20 @@ __global__ __launch_bounds__(C::THREADS) void mx_few_kernel(const Params p, int 
     for (int q = 1; q < W; ++q) y += red[(q * NT * MT + u) * kWave + lane];
     const int m = 16 * (u % MT) + c;
     if (m >= M) continue;
+    if (apart) {
+      for (int e = 0; e < 4; ++e) {
+        const int col = min(n0 + 16 * (u / MT) + 4 * g + e, N - 1);
+        float v = y[e] * p.wcscale[col];
+        for (int r = 0; r < R; ++r)
+          v += widen<F16>(p.lora_act_in[uint32_t(m) * uint32_t(R) + uint32_t(r)]) *
+               widen<F16>(p.lora_up[uint32_t(r) * uint32_t(N) + uint32_t(col)]);
+        y[e] = v;
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int col = n0 + 16 * (u / MT) + 4 * g + e;
-      if (col >= end) continue;
-      float v = y[e];
-      if (apart) {
-        v *= p.wcscale[col];
-        for (int r = 0; r < R; ++r)
-          v += widen<F16>(p.lora_act_in[uint32_t(m) * uint32_t(R) + uint32_t(r)]) * widen<F16>(p.lora_up[uint32_t(r) * uint32_t(N) + uint32_t(col)]);
-      }
-      p.out[uint32_t(m) * uint32_t(N) + uint32_t(col)] = narrow<F16>(v + p.bias[col]);
+      if (col < end) p.out[uint32_t(m) * uint32_t(N) + uint32_t(col)] = narrow<F16>(y[e] + p.bias[col]);
     }
   }
 }
