@@ -11,7 +11,8 @@ Python binding over the C ABI of libgemm_w4a4.so (include/gemm_w4a4.h).
 Around them, for a transformer block on MXFP4 weights: quantize_mxfp4_act (the
 MXFP4 producer), gemm_mxfp4_few (the MXFP4 layer for few rows), rotary_axes
 (rotary positions over several axes) and cross_attention (attention to keys of
-another length).
+another length). For many requests at once: block_norm (norms with gate and
+residual) and cache_append (keys and values into a paged cache).
 
 PyTorch supplies device memory and the stream; every step of the operator runs
 in the library's HIP kernels. If the library is missing the calls raise.
@@ -23,6 +24,7 @@ from ._native import (ATTENTION_MAX_HEAD_DIM, FEW_MAX_M, ROTARY_MAX_AXES, ROTARY
                       AttentionArgs, RotaryArgs,
                       cross_attention_raw, cross_attention_workspace, gemm_mxfp4_few_raw, quantize_mxfp4_raw,
                       quantize_mxfp4_workspace, rotary_axes_raw)
+from ._native import BLOCK_NORM_MAX_WIDTH, BlockNormArgs, CacheAppendArgs, block_norm_raw, cache_append_raw
 from ._native import (EALIGN, EDEVICE, EINVAL, ENOMEM, ESCRATCH, ELAUNCH, EOVERLAP, FORMATS, MAX_R, OK, QUANTIZE_MAX_R,
                       quantize_noalloc_raw, quantize_plan, quantize_raw,
                       gemm_mxfp4_f16_raw, gemm_mxfp4_raw, gemm_w4a4_f16_raw, gemm_w4a4_raw,
@@ -32,6 +34,8 @@ __all__ = ["quantize_mxfp4_act", "gemm_mxfp4_few", "rotary_axes", "cross_attenti
            "quantize_mxfp4_workspace", "gemm_mxfp4_few_raw", "rotary_axes_raw", "cross_attention_raw",
            "cross_attention_workspace", "RotaryArgs", "AttentionArgs", "FEW_MAX_M", "ROTARY_MAX_AXES",
            "ROTARY_MAX_HEAD_DIM", "ATTENTION_MAX_HEAD_DIM",
+           "block_norm", "cache_append", "block_norm_raw", "cache_append_raw", "BlockNormArgs", "CacheAppendArgs",
+           "BLOCK_NORM_MAX_WIDTH",
            "gemm_w4a4", "gemm_mxfp4", "quantize_w4a4_act", "quantize_raw", "quantize_noalloc_raw", "quantize_plan", "QUANTIZE_MAX_R", "gemm_w4a4_raw", "gemm_w4a4_f16_raw", "gemm_mxfp4_raw",
            "gemm_mxfp4_f16_raw", "run_raw", "plan", "plan_variant", "variants", "strerror", "library_path", "GemmError", "OK",
            "EINVAL", "EALIGN", "ELAUNCH", "EOVERLAP", "EDEVICE", "ENOMEM", "ESCRATCH", "MAX_R", "FORMATS"]
@@ -246,6 +250,44 @@ def rotary_axes(x, positions, inv_freq, sections, interleaved=True, inverse=Fals
     itself for in place. Returns out.
     """
     return _run("rotary_axes", stream, x, positions, inv_freq, sections, interleaved, inverse, out)
+
+
+def block_norm(x, y=None, gate=None, residual_scale=1.0, post_norm=False, post_weight=None, kind="layer", weight=None,
+               bias=None, scale=None, shift=None, eps=1e-6, out=None, residual=None, stream=None):
+    """Enqueue the norms after and before a block with its gate and residual in between on `stream`:
+
+        z        = norm(y) * post_weight if post_norm else y
+        residual = residual_scale * x + gate * z
+        out      = (norm(residual) * weight + bias) * (1 + scale) + shift
+
+    x, y bfloat16 or float16 [batch, tokens, width] or [tokens, width], any strides with
+    a dense last dimension, width up to BLOCK_NORM_MAX_WIDTH; kind: "layer", or "rms" for
+    the norm without the mean. gate, scale and shift of x's type: any shape that
+    broadcasts to x's and has its width ([width] or [batch, 1, width] for vectors of all tokens or
+    of a sequence's, x's own for one a token), slices of one tensor too; weight, bias and
+    post_weight [width] of x's type; each is left out when None. Without y, out is the norm
+    of x, and gate, post_norm, residual and residual_scale are not given.
+    eps: 1e-12 .. 1. Float32 throughout; the results are rounded once each, out
+    taken from the residual before its rounding. out and residual: allocated (dense)
+    when None; either may be x or y itself for in place. Returns (out, residual), residual None
+    without y. No gradient is recorded.
+    """
+    return _run("block_norm", stream, x, y, gate, residual_scale, post_norm, post_weight, kind, weight, bias, scale,
+                shift, eps, out, residual)
+
+
+def cache_append(k, v, k_cache, v_cache, slots, stream=None):
+    """Enqueue the keys and values of new tokens into a paged cache on `stream`.
+
+    k, v [tokens, heads, head_dim], k_cache, v_cache [pages, page_size, heads,
+    head_dim] of the same 16-bit type, any strides that are multiples of 8 with a
+    dense last dimension (the caches may be slices of one tensor); head_dim a multiple of
+    8 up to ATTENTION_MAX_HEAD_DIM. slots int64 [tokens] on the device: page * page_size +
+    place of each token; slots outside the cache (-1: padding) are left out. They must differ
+    from each other: of tokens with the same slot any may stay, or parts of several.
+    Returns (k_cache, v_cache), changed in place. No gradient is recorded.
+    """
+    return _run("cache_append", stream, k, v, k_cache, v_cache, slots)
 
 
 def cross_attention(q, k, v, kv_lens=None, scale=None, return_lse=False, out=None, stream=None):

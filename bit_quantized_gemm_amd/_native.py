@@ -62,6 +62,25 @@ class AttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_int64)]
 
 
+class BlockNormArgs(ctypes.Structure):
+    """block_norm_t."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("x", "y", "gate", "scale", "shift", "weight", "bias", "post_weight",
+                                               "out", "residual")] + \
+               [(f, ctypes.c_int) for f in ("batch", "tokens", "width")] + \
+               [(f, ctypes.c_int64 * 2) for f in ("x_stride", "y_stride", "gate_stride", "scale_stride", "shift_stride",
+                                                  "out_stride", "residual_stride")] + \
+               [("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)] + \
+               [(f, ctypes.c_int) for f in ("layer", "post_norm", "f16")]
+
+
+class CacheAppendArgs(ctypes.Structure):
+    """cache_append_t."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("k", "v", "k_cache", "v_cache", "slots")] + \
+               [(f, ctypes.c_int) for f in ("tokens", "heads", "head_dim", "pages", "page_size")] + \
+               [(f, ctypes.c_int64 * 2) for f in ("k_stride", "v_stride")] + \
+               [(f, ctypes.c_int64 * 3) for f in ("k_cache_stride", "v_cache_stride")]
+
+
 class Plan(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int) for f in _PLAN_FIELDS]
 
@@ -134,6 +153,9 @@ def load() -> ctypes.CDLL:
         lib.cross_attention.restype = i
         lib.cross_attention_workspace.argtypes = [vp]
         lib.cross_attention_workspace.restype = i64
+        for name in ("block_norm", "cache_append"):
+            getattr(lib, name).argtypes = [vp, vp]
+            getattr(lib, name).restype = i
         lib.gemm_w4a4_strerror.argtypes = [i]
         lib.gemm_w4a4_strerror.restype = ctypes.c_char_p
         _lib = lib
@@ -208,6 +230,7 @@ FEW_MAX_M = 64
 ROTARY_MAX_AXES = 4
 ROTARY_MAX_HEAD_DIM = 256
 ATTENTION_MAX_HEAD_DIM = 128
+BLOCK_NORM_MAX_WIDTH = 16384
 
 
 def quantize_mxfp4_raw(f16, x, lora_down, act, ascales, lora_act_in, M, K, R, workspace, workspace_bytes,
@@ -245,6 +268,16 @@ def cross_attention_raw(args: "AttentionArgs", stream) -> int:
 def cross_attention_workspace(args: "AttentionArgs") -> int:
     """Workspace bytes of a cross_attention call, or a negative code (host only)."""
     return load().cross_attention_workspace(ctypes.byref(args))
+
+
+def block_norm_raw(args: "BlockNormArgs", stream) -> int:
+    """Direct call of block_norm; returns its code."""
+    return load().block_norm(ctypes.byref(args), stream)
+
+
+def cache_append_raw(args: "CacheAppendArgs", stream) -> int:
+    """Direct call of cache_append; returns its code."""
+    return load().cache_append(ctypes.byref(args), stream)
 
 
 def quantize_plan(M: int, K: int, R: int) -> dict:

@@ -378,6 +378,142 @@ PyObject* attention(PyObject* const* a) {
   return r;
 }
 
+// Strides (batch, token) of a tensor that broadcasts to [batch,] tokens, width.
+void row_strides(int64_t (&to)[2], const Tensor& t, const char* name, const Tensor& x) {
+  const int64_t dims = t.dim(), width = x.size(-1);
+  if (t.scalar_type() != x.scalar_type())
+    raise(PyExc_TypeError, std::string(name) + " must be " + type_text(x.scalar_type()) + ", got " + type_text(t.scalar_type()));
+  bool fit = dims >= 1 && dims <= x.dim() && t.size(-1) == width;
+  for (int64_t i = 2; fit && i <= dims; ++i) fit = t.size(-i) == 1 || t.size(-i) == x.size(-i);
+  if (!fit) raise(PyExc_ValueError, std::string(name) + " of shape " + shape_text(t.sizes()) + " does not broadcast to " + shape_text(x.sizes()));
+  if (t.device() != x.device()) raise(PyExc_ValueError, std::string(name) + " is on " + t.device().str() + ", expected " + x.device().str());
+  if (width > 1 && t.stride(-1) != 1) raise(PyExc_ValueError, std::string("the last dimension of ") + name + " must be dense");
+  for (int64_t i = 0; i < 2; ++i)   // token, batch
+    to[1 - i] = dims >= i + 2 && t.size(-2 - i) > 1 ? t.stride(-2 - i) : 0;
+}
+
+PyObject* norm(PyObject* const* a) {
+  const Tensor& x = tensor(a[0], "x");
+  block_norm_t n{};
+  n.f16 = half_of(x, "x");
+  if (x.dim() != 2 && x.dim() != 3) raise(PyExc_ValueError, "x must be [batch, tokens, width] or [tokens, width]");
+  n.batch = x.dim() == 3 ? dim_of(x.size(0), "x") : 1;
+  n.tokens = dim_of(x.size(-2), "x");
+  n.width = dim_of(x.size(-1), "x");
+  const bool kept = a[1] != Py_None;   // there is a residual
+  auto rows = [&](PyObject* o, const char* name, const void*& to, int64_t (&stride)[2]) {
+    if (o == Py_None) return;
+    const Tensor& t = tensor(o, name);
+    row_strides(stride, t, name, x);
+    to = t.data_ptr();
+  };
+  rows(a[0], "x", n.x, n.x_stride);
+  if (kept) {
+    const Tensor& y = tensor(a[1], "y");
+    same_kind(y, "y", x, x.sizes());
+    rows(a[1], "y", n.y, n.y_stride);
+  }
+  rows(a[2], "gate", n.gate, n.gate_stride);
+  n.residual_scale = float(PyFloat_AsDouble(a[3]));
+  if (PyErr_Occurred()) throw Raised{};
+  n.post_norm = truth(a[4]);
+  auto vec = [&](PyObject* o, const char* name, const void*& to) {
+    if (o == Py_None) return;
+    const Tensor& t = tensor(o, name);
+    want(t, name, x.scalar_type(), {n.width}, x.get_device());
+    to = t.data_ptr();
+  };
+  vec(a[5], "post_weight", n.post_weight);
+  const char* kind = PyUnicode_Check(a[6]) ? PyUnicode_AsUTF8(a[6]) : nullptr;
+  if (PyErr_Occurred()) throw Raised{};
+  const std::string named = kind ? kind : "";
+  if (named != "layer" && named != "rms") raise(PyExc_ValueError, "kind must be \"layer\" or \"rms\"");
+  n.layer = named == "layer";
+  vec(a[7], "weight", n.weight);
+  vec(a[8], "bias", n.bias);
+  rows(a[9], "scale", n.scale, n.scale_stride);
+  rows(a[10], "shift", n.shift, n.shift_stride);
+  n.eps = float(PyFloat_AsDouble(a[11]));
+  if (PyErr_Occurred()) throw Raised{};
+  if (!kept && (n.gate || n.post_norm || a[13] != Py_None || n.residual_scale != 1.f))
+    raise(PyExc_ValueError, "gate, residual_scale, post_norm and residual need y");
+  if (n.post_weight && !n.post_norm) raise(PyExc_ValueError, "post_weight needs post_norm");
+  auto result = [&](PyObject* o, const char* name) {
+    if (o == Py_None) return empty(x.sizes(), x.scalar_type(), x.device());
+    const Tensor& t = tensor(o, name);
+    same_kind(t, name, x, x.sizes());
+    return t;
+  };
+  const Tensor out = result(a[12], "out");
+  row_strides(n.out_stride, out, "out", x);
+  n.out = out.data_ptr();
+  Tensor res;
+  if (kept) {
+    res = result(a[13], "residual");
+    row_strides(n.residual_stride, res, "residual", x);
+    n.residual = res.data_ptr();
+  }
+  const OnDevice on(x.device());
+  const int rc = block_norm(&n, on.stream);
+  if (rc != GEMM_W4A4_OK) return PyLong_FromLong(rc);
+  written(a[12]);
+  if (kept) written(a[13]);
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, wrap(out));
+  PyTuple_SET_ITEM(r, 1, kept ? wrap(res) : Py_NewRef(Py_None));
+  return r;
+}
+
+// Caches [pages, page_size, heads, head_dim] of one shape, like x but for the device check's name.
+void caches(const Tensor& k, const Tensor& v, const Tensor& x) {
+  if (k.dim() != 4) raise(PyExc_ValueError, "k_cache must be [pages, page_size, heads, head_dim]");
+  same_kind(k, "k_cache", x, k.sizes());
+  same_kind(v, "v_cache", x, k.sizes());
+}
+
+PyObject* append(PyObject* const* a) {
+  const Tensor& k = tensor(a[0], "k");
+  const Tensor& v = tensor(a[1], "v");
+  const Tensor& kc = tensor(a[2], "k_cache");
+  const Tensor& vc = tensor(a[3], "v_cache");
+  const Tensor& slots = tensor(a[4], "slots");
+  half_of(k, "k");
+  if (k.dim() != 3) raise(PyExc_ValueError, "k and v must be [tokens, heads, head_dim]");
+  same_kind(v, "v", k, k.sizes());
+  caches(kc, vc, k);
+  if (kc.size(2) != k.size(1) || kc.size(3) != k.size(2))
+    raise(PyExc_ValueError, "k_cache has heads of " + shape_text(kc.sizes().slice(2)) + ", k of " + shape_text(k.sizes().slice(1)));
+  want(slots, "slots", at::kLong, {k.size(0)}, k.get_device());
+  cache_append_t c{};
+  c.tokens = dim_of(k.size(0), "k");
+  c.heads = dim_of(k.size(1), "k");
+  c.head_dim = dim_of(k.size(2), "k");
+  c.pages = dim_of(kc.size(0), "k_cache");
+  c.page_size = dim_of(kc.size(1), "k_cache");
+  const struct { const Tensor& t; const char* name; int64_t* to; int outer; } strided[] = {
+      {k, "k", c.k_stride, 2}, {v, "v", c.v_stride, 2}, {kc, "k_cache", c.k_cache_stride, 3}, {vc, "v_cache", c.v_cache_stride, 3}};
+  for (const auto& s : strided) {
+    if (s.t.stride(s.outer) != 1) raise(PyExc_ValueError, std::string("the last dimension of ") + s.name + " must be dense");
+    for (int i = 0; i < s.outer; ++i) s.to[i] = s.t.stride(i);
+  }
+  c.k = k.data_ptr();
+  c.v = v.data_ptr();
+  c.k_cache = kc.data_ptr();
+  c.v_cache = vc.data_ptr();
+  c.slots = ptr<int64_t>(slots);
+  const OnDevice on(k.device());
+  const int rc = cache_append(&c, on.stream);
+  if (rc != GEMM_W4A4_OK) return PyLong_FromLong(rc);
+  written(a[2]);
+  written(a[3]);
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, wrap(kc));
+  PyTuple_SET_ITEM(r, 1, wrap(vc));
+  return r;
+}
+
 // ---------------------------------------------------------------- the module
 
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -406,6 +542,8 @@ PyMethodDef g_methods[] = {
     method<few, 10>("gemm_mxfp4_few"),           // act .. lora_up, out, dtype
     method<rotary, 7>("rotary_axes"),            // x, positions, inv_freq, sections, interleaved, inverse, out
     method<attention, 7>("cross_attention"),     // q, k, v, kv_lens, scale, return_lse, out
+    method<norm, 14>("block_norm"),              // x .. shift, eps, out, residual
+    method<append, 5>("cache_append"),           // k, v, k_cache, v_cache, slots
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -10,9 +10,11 @@ namespace w4a4 {
 
 // Whether dimensions of these sizes and strides (elements, run of `run`
 // dense elements inside) give every index memory of its own.
-inline bool strides_apart(const int (&size)[3], const int64_t (&stride)[3], int64_t run) {
-  int order[3] = {0, 1, 2};
-  std::sort(order, order + 3, [&](int a, int b) { return stride[a] < stride[b]; });
+template <int N>
+inline bool strides_apart(const int (&size)[N], const int64_t (&stride)[N], int64_t run) {
+  int order[N];
+  for (int i = 0; i < N; ++i) order[i] = i;
+  std::sort(order, order + N, [&](int a, int b) { return stride[a] < stride[b]; });
   int64_t span = run;
   for (int i : order) {
     if (size[i] <= 1) continue;

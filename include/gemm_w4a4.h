@@ -496,6 +496,91 @@ int cross_attention(const cross_attention_t* args, void* stream);
  * pointer is read), or GEMM_W4A4_EINVAL (host only). */
 int64_t cross_attention_workspace(const cross_attention_t* args);
 
+/*
+ * block_norm — the norms after and before a block with its gate and residual in
+ * between, on rows x and y [batch, tokens, width]:
+ *
+ *     z        = post_norm ? norm(y) * post_weight : y
+ *     residual = residual_scale * x + gate * z
+ *     out      = (norm(residual) * weight + bias) * (1 + scale) + shift
+ *
+ * norm(v) is (v - mean) / sqrt(var + eps) over the row (layer; var the mean of
+ * the squared differences) or v / sqrt(mean of v^2 + eps). Without y, out is the norm of
+ * x; residual, gate and post_norm are then not given and residual_scale is 1
+ * (GEMM_W4A4_EINVAL). gate, scale, shift, weight, bias and post_weight may
+ * each be NULL: left out. residual may be NULL: not written.
+ *
+ * All float32 from the 16-bit inputs to the two results, each rounded once: out
+ * follows from the residual as it was before its rounding. Rows whose squares
+ * pass float32's range have the result that they have in exact arithmetic; a row
+ * with an infinity or a NaN has NaN as torch's would.
+ *
+ * width 1 .. BLOCK_NORM_MAX_WIDTH, odd ones too; batch * tokens below 2^31; eps 1e-12 .. 1;
+ * residual_scale finite. Strides in elements, non-negative, the last dimension dense;
+ * all tensors 2-byte aligned. gate, scale and shift have strides of their own
+ * (0: one vector for the batch or for all tokens) and may be slices of one
+ * tensor. out and residual may not make two rows share memory; each may be x
+ * or y itself with the same strides (in place); otherwise the memory from its first to
+ * its last element may hold nothing of an input or of the other
+ * (GEMM_W4A4_EOVERLAP). batch or tokens 0: nothing is enqueued.
+ * No workspace; deterministic.
+ */
+#define BLOCK_NORM_MAX_WIDTH 16384
+typedef struct {
+  const void* x;             /* 16-bit type, see f16 */
+  const void* y;
+  const void* gate;
+  const void* scale;
+  const void* shift;
+  const void* weight;        /* [width], as bias and post_weight */
+  const void* bias;
+  const void* post_weight;
+  void* out;
+  void* residual;
+  int batch, tokens, width;
+  int64_t x_stride[2];       /* batch, token */
+  int64_t y_stride[2];
+  int64_t gate_stride[2];
+  int64_t scale_stride[2];
+  int64_t shift_stride[2];
+  int64_t out_stride[2];
+  int64_t residual_stride[2];
+  float residual_scale, eps;
+  int layer;                 /* 1: the layer norm, 0: without the mean */
+  int post_norm;
+  int f16;                   /* 0: bfloat16, 1: binary16 */
+} block_norm_t;
+int block_norm(const block_norm_t* args, void* stream);
+
+/*
+ * cache_append — keys and values of new tokens, k and v [tokens, heads,
+ * head_dim], into a paged cache, k_cache and v_cache [pages, page_size, heads,
+ * head_dim]: token t goes to place slots[t] % page_size of page slots[t] / page_size.
+ * Slots outside 0 .. pages * page_size - 1 are left out (padding: -1). The slots of
+ * a call's tokens must differ from each other: of two tokens with one slot either may stay, or
+ * a part of each. Nothing else of the cache changes.
+ *
+ * tokens up to 2^30; head_dim a multiple of 8, 8 .. CROSS_ATTENTION_MAX_HEAD_DIM; fewer than
+ * 2^20 heads; pages * page_size below 2^31. Strides in elements, multiples of 8
+ * (a dimension of size 1 excepted), non-negative, the last dimension dense; tensors 16-byte,
+ * slots 8-byte aligned. k and v may repeat memory; a cache may not, and may overlap nothing
+ * else. Both caches may lie in one buffer (a page of the one beside a page of the
+ * other) with the same strides. tokens or pages 0: nothing is enqueued.
+ */
+typedef struct {
+  const void* k;             /* 16-bit values of any type */
+  const void* v;
+  void* k_cache;
+  void* v_cache;
+  const int64_t* slots;      /* [tokens] on the device */
+  int tokens, heads, head_dim, pages, page_size;
+  int64_t k_stride[2];       /* token, head */
+  int64_t v_stride[2];
+  int64_t k_cache_stride[3]; /* page, token, head */
+  int64_t v_cache_stride[3];
+} cache_append_t;
+int cache_append(const cache_append_t* args, void* stream);
+
 /* Static string for a return code (never NULL). */
 const char* gemm_w4a4_strerror(int code);
 

@@ -1,0 +1,75 @@
+"""Plain CPU oracles of the operators that serve many requests at once, in
+float64, each with the error bound its kernel is held to.
+
+TEST INFRASTRUCTURE ONLY. The product (``bit_quantized_gemm_amd``) never
+imports it and shares no code with it.
+
+Tensors come as float64 arrays of the 16-bit inputs' values, with dtype "bf16"
+or "f16".
+"""
+from __future__ import annotations
+
+import numpy as np
+
+from .block_ref import half_spacing
+
+__all__ = ["block_norm_ref", "cache_append_ref"]
+
+# relative error of a float32 sum of a row: at most 64 additions in a lane and 12
+# across lanes and waves, each off by 2^-24 of the partial sum
+SUM = 76 * 2.0 ** -24
+
+
+def _norm(v, layer, eps, err):
+    """norm(v), and how far the kernel's may be off when its v is off by at most err."""
+    mean = v.mean(-1, keepdims=True) if layer else 0.0
+    d = v - mean
+    rstd = 1.0 / np.sqrt((d * d).mean(-1, keepdims=True) + eps)
+    n = d * rstd
+    size = np.abs(v).mean(-1, keepdims=True)
+    # of the mean: SUM of the mean magnitude, and v's own error; the difference and the
+    # product round once each (2^-24), the square root and the division within 2^-21 together
+    of_mean = (SUM * size + err.mean(-1, keepdims=True)) if layer else 0.0
+    of_d = of_mean + err + 2.0 ** -23 * np.abs(v)
+    # of 1 / sqrt(var + eps), relative: half of the sum's, of the common shift's and of v's
+    rms = np.sqrt((of_d * of_d).mean(-1, keepdims=True))
+    of_rstd = SUM + rms * rstd + 2.0 ** -21
+    return n, rstd * of_d * (1 + of_rstd) + np.abs(n) * of_rstd
+
+
+def block_norm_ref(x, y=None, gate=None, residual_scale=1.0, post_norm=False, post_weight=None, layer=True, weight=None,
+                   bias=None, scale=None, shift=None, eps=1e-6, dtype="bf16"):
+    """x, y [..., width], the others broadcast to it -> (out, residual, bounds of both)."""
+    u = 2.0 ** -24
+    one = np.ones_like(x)
+    r, err = x.copy(), np.zeros_like(x)
+    if y is not None:
+        z, ez = y.copy(), np.zeros_like(x)
+        if post_norm:
+            z, ez = _norm(y, layer, eps, ez)
+            w = one if post_weight is None else post_weight
+            z, ez = z * w, ez * np.abs(w) + 2 * u * np.abs(z * w)
+        g = one if gate is None else gate
+        z, ez = z * g, ez * np.abs(g) + 2 * u * np.abs(z * g)
+        a = float(np.float32(residual_scale))
+        r = a * x + z
+        err = ez + 2 * u * (np.abs(a * x) + np.abs(z))
+    n, en = _norm(r, layer, eps, err)
+    for factor, term in ((weight, bias), (None if scale is None else 1 + scale, shift)):
+        f = one if factor is None else factor
+        t = 0.0 if term is None else term
+        # (1 + scale is not rounded by itself: n + n scale, two roundings)
+        en = en * np.abs(f) + 4 * u * (np.abs(n) * (1 + np.abs(f)) + np.abs(t))
+        n = n * f + t
+    return n, r, en + 0.5 * half_spacing(n, dtype) * (1 + 2.0 ** -6), err + 0.5 * half_spacing(r, dtype) * (1 + 2.0 ** -6)
+
+
+def cache_append_ref(k, v, k_cache, v_cache, slots):
+    """The caches [pages, page_size, heads, head_dim] after the tokens k, v [tokens, heads, head_dim] (any dtype)."""
+    kc, vc = k_cache.copy(), v_cache.copy()
+    pages, page = kc.shape[:2]
+    for t, s in enumerate(slots):
+        if 0 <= s < pages * page:
+            kc[s // page, s % page] = k[t]
+            vc[s // page, s % page] = v[t]
+    return kc, vc

@@ -1,0 +1,125 @@
+"""What the operators for many requests refuse, before anything is enqueued (CPU: no call
+here reaches a launch), and that their structures match the header."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+import bit_quantized_gemm_amd as w4
+
+REACHED = (w4.OK, w4.EDEVICE, w4.ELAUNCH)   # checks passed; only the device check is left here
+
+
+# ---------------------------------------------------------------- block_norm
+
+def norm(**over):
+    a = dict(x=0x10000000, y=0x20000000, gate=0x30000000, scale=0x31000000, shift=0x32000000, weight=0x33000000, bias=0x34000000,
+             post_weight=0x35000000, out=0x40000000, residual=0x50000000, batch=2, tokens=7, width=100, x_stride=(700, 100),
+             y_stride=(700, 100), gate_stride=(100, 0), scale_stride=(100, 0), shift_stride=(0, 0), out_stride=(700, 100),
+             residual_stride=(700, 100), residual_scale=1.0, eps=1e-6, layer=1, post_norm=1, f16=0)
+    a.update(over)
+    return w4.block_norm_raw(w4.BlockNormArgs(*a.values()), 0)
+
+
+NO_Y = dict(y=0, gate=0, residual=0, post_norm=0, post_weight=0)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(batch=-1), "EINVAL"), (dict(tokens=-1), "EINVAL"), (dict(width=0), "EINVAL"), (dict(width=16385), "EINVAL"),
+    (dict(f16=2), "EINVAL"), (dict(layer=2), "EINVAL"), (dict(post_norm=-1), "EINVAL"), (dict(eps=0.0), "EINVAL"),
+    (dict(eps=-1e-6), "EINVAL"), (dict(eps=2.0), "EINVAL"), (dict(eps=float("nan")), "EINVAL"),
+    (dict(residual_scale=float("inf")), "EINVAL"), (dict(residual_scale=float("nan")), "EINVAL"),
+    (dict(batch=1 << 16, tokens=1 << 15), "EINVAL"), (dict(y=0), "EINVAL"), (dict(NO_Y, gate=0x30000000), "EINVAL"),
+    (dict(NO_Y, residual=0x50000000), "EINVAL"), (dict(NO_Y, post_norm=1), "EINVAL"), (dict(NO_Y, residual_scale=2.0), "EINVAL"),
+    (dict(post_norm=0), "EINVAL"), (dict(x_stride=(700, -100)), "EINVAL"), (dict(gate_stride=(1 << 61, 0)), "EINVAL"),
+    (dict(out_stride=(700, 0)), "EINVAL"), (dict(out_stride=(0, 100)), "EINVAL"), (dict(residual_stride=(700, 99)), "EINVAL"),
+    (dict(x=0), "EINVAL"), (dict(out=0), "EINVAL"), (dict(x=0x10000001), "EALIGN"), (dict(weight=0x33000001), "EALIGN"),
+    (dict(residual=0x50000001), "EALIGN"), (dict(out=0x10000002), "EOVERLAP"), (dict(out=0x20000000, out_stride=(1400, 200)), "EOVERLAP"),
+    (dict(residual=0x40000010), "EOVERLAP"), (dict(residual=0x40000000), "EOVERLAP"), (dict(gate=0x40000000), "EOVERLAP"),
+    (dict(shift=0x50000100), "EOVERLAP"), (dict(weight=0x40000002), "EOVERLAP"), (dict(post_weight=0x50000002), "EOVERLAP")])
+def test_norm_refuses(over, code):
+    assert norm(**over) == getattr(w4, code)
+
+
+@pytest.mark.parametrize("over", [
+    dict(), NO_Y, dict(NO_Y, out=0x10000000), dict(out=0x10000000, residual=0x20000000), dict(residual=0x10000000),
+    dict(residual=0), dict(gate=0, scale=0, shift=0, weight=0, bias=0, post_weight=0), dict(post_norm=0, post_weight=0),
+    dict(x_stride=(0, 0)), dict(scale_stride=(700, 100)), dict(batch=1, out_stride=(0, 100)), dict(width=1, out_stride=(7, 1))])
+def test_norm_accepts(over):
+    assert norm(**over) in REACHED
+
+
+def test_norm_empty_and_null():
+    assert norm(batch=0) == w4.OK and norm(tokens=0, x=0, out=0) == w4.OK
+    assert w4._native.load().block_norm(None, None) == w4.EINVAL
+
+
+# ---------------------------------------------------------------- cache_append
+
+def append(**over):
+    a = dict(k=0x10000000, v=0x20000000, k_cache=0x30000000, v_cache=0x40000000, slots=0x50000000, tokens=10, heads=4, head_dim=64,
+             pages=5, page_size=16, k_stride=(256, 64), v_stride=(256, 64), k_cache_stride=(4096, 256, 64), v_cache_stride=(4096, 256, 64))
+    a.update(over)
+    return w4.cache_append_raw(w4.CacheAppendArgs(*a.values()), 0)
+
+
+ONE = dict(k_cache_stride=(8192, 256, 64), v_cache_stride=(8192, 256, 64))
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(tokens=-1), "EINVAL"), (dict(tokens=(1 << 30) + 1), "EINVAL"), (dict(heads=0), "EINVAL"), (dict(heads=1 << 20), "EINVAL"),
+    (dict(head_dim=0), "EINVAL"), (dict(head_dim=12), "EINVAL"), (dict(head_dim=136), "EINVAL"), (dict(pages=-1), "EINVAL"),
+    (dict(page_size=0), "EINVAL"), (dict(pages=1 << 20, page_size=1 << 11), "EINVAL"), (dict(k_stride=(256, -64)), "EINVAL"),
+    (dict(v_stride=(260, 64)), "EINVAL"), (dict(k_cache_stride=(4096, 256, 32)), "EINVAL"), (dict(v_cache_stride=(0, 256, 64)), "EINVAL"),
+    (dict(k_cache_stride=(4096, 260, 64)), "EINVAL"), (dict(k=0), "EINVAL"), (dict(v_cache=0), "EINVAL"), (dict(slots=0), "EINVAL"),
+    (dict(k=0x10000008), "EALIGN"), (dict(v_cache=0x40000002), "EALIGN"), (dict(slots=0x50000004), "EALIGN"),
+    (dict(k=0x30000010), "EOVERLAP"), (dict(slots=0x40000008), "EOVERLAP"), (dict(v_cache=0x30000000), "EOVERLAP"),
+    (dict(v_cache=0x30000080), "EOVERLAP"), (dict(ONE, v_cache=0x30001000), "EOVERLAP"),
+    (dict(v_cache=0x30002000, k_cache_stride=(8192, 256, 64), v_cache_stride=(8192, 512, 64)), "EOVERLAP")])
+def test_append_refuses(over, code):
+    assert append(**over) == getattr(w4, code)
+
+
+@pytest.mark.parametrize("over", [
+    dict(), dict(k_stride=(0, 0)), dict(v=0x10000000), dict(ONE, v_cache=0x30002000), dict(tokens=1, k_stride=(3, 64)),
+    dict(page_size=1, k_cache_stride=(256, 7, 64), v_cache_stride=(256, 7, 64))])
+def test_append_accepts(over):
+    assert append(**over) in REACHED
+
+
+def test_append_empty_and_null():
+    assert append(tokens=0, k=0) == w4.OK and append(pages=0, k_cache=0, v_cache=0) == w4.OK
+    assert w4._native.load().cache_append(None, None) == w4.EINVAL
+
+
+# ---------------------------------------------------------------- the Python checks
+
+def test_python_checks():
+    bf, z = torch.bfloat16, torch.zeros
+    with pytest.raises(TypeError):
+        w4.block_norm(z(4, 32))
+    with pytest.raises(ValueError):
+        w4.block_norm(z(4, 32, dtype=bf))                              # not on a GPU
+    with pytest.raises(ValueError):
+        w4.cache_append(*(z(1, 1, 8, dtype=bf) for _ in range(4)), z(1, dtype=torch.int64))
+
+
+STRUCTURES = {"block_norm_t": "BlockNormArgs", "cache_append_t": "CacheAppendArgs"}
+
+
+def test_structures_match_the_header(tmp_path):
+    """Field offsets of the ctypes structures equal those a C compiler gives the header's."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    names = {t: getattr(w4, c) for t, c in STRUCTURES.items()}
+    body = "".join(f'printf("%zu\\n", sizeof({t}));' + "".join(f'printf("%zu\\n", offsetof({t}, {f[0]}));' for f in c._fields_)
+                   for t, c in names.items())
+    src = tmp_path / "t.c"
+    src.write_text("#include <stddef.h>\n#include <stdio.h>\n#include \"gemm_w4a4.h\"\nint main(void) {" + body + "return 0;}")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", f"-I{root}/include", str(src), "-o", str(tmp_path / "t")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "t")], capture_output=True, text=True, check=True).stdout.split()]
+    want = []
+    for c in names.values():
+        want += [ctypes.sizeof(c)] + [getattr(c, f[0]).offset for f in c._fields_]
+    assert got == want
