@@ -12,7 +12,8 @@ Around them, for a transformer block on MXFP4 weights: quantize_mxfp4_act (the
 MXFP4 producer), gemm_mxfp4_few (the MXFP4 layer for few rows), rotary_axes
 (rotary positions over several axes) and cross_attention (attention to keys of
 another length). For many requests at once: block_norm (norms with gate and
-residual) and cache_append (keys and values into a paged cache).
+residual), lora_adapters (each request's own low-rank adapter beside a shared
+projection) and cache_append (keys and values into a paged cache).
 
 PyTorch supplies device memory and the stream; every step of the operator runs
 in the library's HIP kernels. If the library is missing the calls raise.
@@ -24,7 +25,9 @@ from ._native import (ATTENTION_MAX_HEAD_DIM, FEW_MAX_M, ROTARY_MAX_AXES, ROTARY
                       AttentionArgs, RotaryArgs,
                       cross_attention_raw, cross_attention_workspace, gemm_mxfp4_few_raw, quantize_mxfp4_raw,
                       quantize_mxfp4_workspace, rotary_axes_raw)
-from ._native import BLOCK_NORM_MAX_WIDTH, BlockNormArgs, CacheAppendArgs, block_norm_raw, cache_append_raw
+from ._native import (BLOCK_NORM_MAX_WIDTH, LORA_ADAPTERS_MAX_RANK, LORA_ADAPTERS_MAX_ROWS,
+                      BlockNormArgs, CacheAppendArgs, LoraAdaptersArgs,
+                      block_norm_raw, cache_append_raw, lora_adapters_raw, lora_adapters_workspace)
 from ._native import (EALIGN, EDEVICE, EINVAL, ENOMEM, ESCRATCH, ELAUNCH, EOVERLAP, FORMATS, MAX_R, OK, QUANTIZE_MAX_R,
                       quantize_noalloc_raw, quantize_plan, quantize_raw,
                       gemm_mxfp4_f16_raw, gemm_mxfp4_raw, gemm_w4a4_f16_raw, gemm_w4a4_raw,
@@ -35,7 +38,8 @@ __all__ = ["quantize_mxfp4_act", "gemm_mxfp4_few", "rotary_axes", "cross_attenti
            "cross_attention_workspace", "RotaryArgs", "AttentionArgs", "FEW_MAX_M", "ROTARY_MAX_AXES",
            "ROTARY_MAX_HEAD_DIM", "ATTENTION_MAX_HEAD_DIM",
            "block_norm", "cache_append", "block_norm_raw", "cache_append_raw", "BlockNormArgs", "CacheAppendArgs",
-           "BLOCK_NORM_MAX_WIDTH",
+           "BLOCK_NORM_MAX_WIDTH", "lora_adapters", "lora_adapters_raw", "lora_adapters_workspace", "LoraAdaptersArgs",
+           "LORA_ADAPTERS_MAX_RANK", "LORA_ADAPTERS_MAX_ROWS",
            "gemm_w4a4", "gemm_mxfp4", "quantize_w4a4_act", "quantize_raw", "quantize_noalloc_raw", "quantize_plan", "QUANTIZE_MAX_R", "gemm_w4a4_raw", "gemm_w4a4_f16_raw", "gemm_mxfp4_raw",
            "gemm_mxfp4_f16_raw", "run_raw", "plan", "plan_variant", "variants", "strerror", "library_path", "GemmError", "OK",
            "EINVAL", "EALIGN", "ELAUNCH", "EOVERLAP", "EDEVICE", "ENOMEM", "ESCRATCH", "MAX_R", "FORMATS"]
@@ -274,6 +278,22 @@ def block_norm(x, y=None, gate=None, residual_scale=1.0, post_norm=False, post_w
     """
     return _run("block_norm", stream, x, y, gate, residual_scale, post_norm, post_weight, kind, weight, bias, scale,
                 shift, eps, out, residual)
+
+
+def lora_adapters(y, x, down, up, adapter, scaling=None, ranks=None, out=None, stream=None):
+    """Enqueue the low-rank adapters of many requests beside a shared projection on `stream`: for every row m,
+    with a = adapter[m], out[m] = y[m] + scaling[a] * (x[m] @ down[a]^T) @ up[a].
+
+    y [rows, N], the projection's result, and x [rows, K], its input (K % 8 == 0), bfloat16 or
+    float16, any row stride (x's a multiple of 8) with a dense last dimension; down
+    [adapters, rank, K] and up [adapters, rank, N] of that type, dense, rank up to
+    LORA_ADAPTERS_MAX_RANK. adapter int32 [rows] on the device; values outside 0 .. adapters - 1:
+    no adapter, out[m] = y[m]. scaling float32 [adapters] (None: 1). ranks int32 [adapters]: ranks in use of each
+    adapter (None: all); what down and up hold from there on does not matter. At most
+    LORA_ADAPTERS_MAX_ROWS rows, in any order (those of one adapter beside each other share its reads).
+    out: allocated (dense) when None; y itself for in place. Returns out. No gradient is recorded.
+    """
+    return _run("lora_adapters", stream, y, x, down, up, adapter, scaling, ranks, out)
 
 
 def cache_append(k, v, k_cache, v_cache, slots, stream=None):

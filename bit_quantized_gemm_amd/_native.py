@@ -81,6 +81,14 @@ class CacheAppendArgs(ctypes.Structure):
                [(f, ctypes.c_int64 * 3) for f in ("k_cache_stride", "v_cache_stride")]
 
 
+class LoraAdaptersArgs(ctypes.Structure):
+    """lora_adapters_t."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("x", "y", "down", "up", "out", "adapter", "scaling", "ranks")] + \
+               [(f, ctypes.c_int) for f in ("rows", "K", "N", "adapters", "rank")] + \
+               [(f, ctypes.c_int64) for f in ("x_stride", "y_stride", "out_stride")] + \
+               [("f16", ctypes.c_int), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
 class Plan(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int) for f in _PLAN_FIELDS]
 
@@ -153,9 +161,11 @@ def load() -> ctypes.CDLL:
         lib.cross_attention.restype = i
         lib.cross_attention_workspace.argtypes = [vp]
         lib.cross_attention_workspace.restype = i64
-        for name in ("block_norm", "cache_append"):
+        for name in ("block_norm", "cache_append", "lora_adapters"):
             getattr(lib, name).argtypes = [vp, vp]
             getattr(lib, name).restype = i
+        lib.lora_adapters_workspace.argtypes = [vp]
+        lib.lora_adapters_workspace.restype = i64
         lib.gemm_w4a4_strerror.argtypes = [i]
         lib.gemm_w4a4_strerror.restype = ctypes.c_char_p
         _lib = lib
@@ -231,6 +241,8 @@ ROTARY_MAX_AXES = 4
 ROTARY_MAX_HEAD_DIM = 256
 ATTENTION_MAX_HEAD_DIM = 128
 BLOCK_NORM_MAX_WIDTH = 16384
+LORA_ADAPTERS_MAX_RANK = 128
+LORA_ADAPTERS_MAX_ROWS = 4194240
 
 
 def quantize_mxfp4_raw(f16, x, lora_down, act, ascales, lora_act_in, M, K, R, workspace, workspace_bytes,
@@ -278,6 +290,16 @@ def block_norm_raw(args: "BlockNormArgs", stream) -> int:
 def cache_append_raw(args: "CacheAppendArgs", stream) -> int:
     """Direct call of cache_append; returns its code."""
     return load().cache_append(ctypes.byref(args), stream)
+
+
+def lora_adapters_raw(args: "LoraAdaptersArgs", stream) -> int:
+    """Direct call of lora_adapters; returns its code."""
+    return load().lora_adapters(ctypes.byref(args), stream)
+
+
+def lora_adapters_workspace(args: "LoraAdaptersArgs") -> int:
+    """Workspace bytes of a lora_adapters call, or a negative code (host only)."""
+    return load().lora_adapters_workspace(ctypes.byref(args))
 
 
 def quantize_plan(M: int, K: int, R: int) -> dict:

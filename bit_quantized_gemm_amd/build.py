@@ -38,7 +38,8 @@ PROBES_LIB_PATH = os.path.join(PKG_DIR, "libw4a4_probes.so")
 # library -> (the sources it is built from, whether it carries the resource table)
 LIBS = {
     LIB_PATH: (("gemm_w4a4.hip", "gemm_mxfp4.hip", "w4a4_producer.hip", "mxfp4_producer.hip",
-                "mxfp4_few.hip", "rotary.hip", "attention.hip", "block_norm.hip", "cache_append.hip"), True),
+                "mxfp4_few.hip", "rotary.hip", "attention.hip", "block_norm.hip", "cache_append.hip",
+                "lora_adapters.hip"), True),
     PROBES_LIB_PATH: (("mfma_peak.hip", "route_probe.hip"), False),
 }
 BINDING_PATH = os.path.join(PKG_DIR, "_torch_binding.so")

@@ -47,6 +47,8 @@
 #include "w4a4_half.hpp"
 #include "w4a4_host.hpp"
 #include "w4a4_strided.hpp"
+#include "w4a4_transpose.hpp"
+#include "w4a4_wave.hpp"
 
 namespace w4a4 {
 
@@ -190,25 +192,6 @@ template <class C>
 __device__ __forceinline__ int k_chunk(int r, int c) { return c ^ (C::CH == 16 ? r & 15 : (r >> 1) & 7); }
 template <class C>
 __device__ __forceinline__ int v_chunk(int r, int c) { return c ^ (C::CH == 16 ? (r & 3) << 2 : ((r >> 1) & 1) << 2); }
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-// Transposed read: the lanes of a group of 16 pass the addresses of 4 rows x 4
-// runs of 4 values; lane i gets column i of the 4 rows.
-__device__ __forceinline__ u32x2 read_transposed(const uint8_t* p) {
-  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                       (__attribute__((address_space(3))) s16x4*)p));
-}
-
-// max(v, v of lane ^ 32); likewise the sum
-__device__ __forceinline__ float other_max(float v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-  return fmaxf(__builtin_bit_cast(float, uint32_t(r[0])), __builtin_bit_cast(float, uint32_t(r[1])));
-}
-__device__ __forceinline__ float other_sum(float v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-  return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
-}
 
 // A weight is exp2(s c - m), s c in one fma with the rounded maximum m, so that
 // the top score's own is 2^r, r the rounding of its product: at most 1 up to this

@@ -465,6 +465,70 @@ PyObject* norm(PyObject* const* a) {
   return r;
 }
 
+PyObject* adapters(PyObject* const* a) {
+  const Tensor& y = tensor(a[0], "y");
+  const Tensor& x = tensor(a[1], "x");
+  const Tensor& down = tensor(a[2], "down");
+  const Tensor& up = tensor(a[3], "up");
+  lora_adapters_t l{};
+  l.f16 = half_of(y, "y");
+  if (y.dim() != 2 || x.dim() != 2 || down.dim() != 3) raise(PyExc_ValueError, "y and x must be 2-D, down and up 3-D");
+  const c10::Device device = y.device();
+  const int index = device.index();
+  l.rows = dim_of(y.size(0), "y");
+  l.N = dim_of(y.size(1), "y");
+  l.K = dim_of(x.size(1), "x");
+  l.adapters = dim_of(down.size(0), "down");
+  l.rank = dim_of(down.size(1), "down");
+  const int64_t xs[2] = {l.rows, l.K};
+  same_kind(x, "x", y, xs);
+  want(down, "down", y.scalar_type(), {l.adapters, l.rank, l.K}, index);
+  want(up, "up", y.scalar_type(), {l.adapters, l.rank, l.N}, index);
+  const Tensor& which = tensor(a[4], "adapter");
+  want(which, "adapter", at::kInt, {l.rows}, index);
+  if (a[5] != Py_None) {
+    const Tensor& s = tensor(a[5], "scaling");
+    want(s, "scaling", at::kFloat, {l.adapters}, index);
+    l.scaling = ptr<float>(s);
+  }
+  if (a[6] != Py_None) {
+    const Tensor& r = tensor(a[6], "ranks");
+    want(r, "ranks", at::kInt, {l.adapters}, index);
+    l.ranks = ptr<int32_t>(r);
+  }
+  Tensor out;
+  if (a[7] == Py_None) {
+    out = empty(y.sizes(), y.scalar_type(), device);
+  } else {
+    out = tensor(a[7], "out");
+    same_kind(out, "out", y, y.sizes());
+  }
+  const struct { const Tensor& t; const char* name; int64_t& to; } strided[] = {
+      {x, "x", l.x_stride}, {y, "y", l.y_stride}, {out, "out", l.out_stride}};
+  for (const auto& s : strided) {
+    if (s.t.size(1) > 1 && s.t.stride(1) != 1) raise(PyExc_ValueError, std::string("the last dimension of ") + s.name + " must be dense");
+    s.to = s.t.stride(0);
+  }
+  l.x = x.data_ptr();
+  l.y = y.data_ptr();
+  l.down = down.data_ptr();
+  l.up = up.data_ptr();
+  l.out = out.data_ptr();
+  l.adapter = ptr<int32_t>(which);
+  const OnDevice on(device);
+  l.workspace_bytes = lora_adapters_workspace(&l);
+  if (l.workspace_bytes < 0) return PyLong_FromLong(long(l.workspace_bytes));
+  Tensor ws;
+  if (l.workspace_bytes > 0) {
+    ws = empty({l.workspace_bytes}, at::kByte, device);
+    l.workspace = ws.data_ptr();
+  }
+  const int rc = lora_adapters(&l, on.stream);
+  if (rc != GEMM_W4A4_OK) return PyLong_FromLong(rc);
+  written(a[7]);
+  return wrap(out);
+}
+
 // Caches [pages, page_size, heads, head_dim] of one shape, like x but for the device check's name.
 void caches(const Tensor& k, const Tensor& v, const Tensor& x) {
   if (k.dim() != 4) raise(PyExc_ValueError, "k_cache must be [pages, page_size, heads, head_dim]");
@@ -543,6 +607,7 @@ PyMethodDef g_methods[] = {
     method<rotary, 7>("rotary_axes"),            // x, positions, inv_freq, sections, interleaved, inverse, out
     method<attention, 7>("cross_attention"),     // q, k, v, kv_lens, scale, return_lse, out
     method<norm, 14>("block_norm"),              // x .. shift, eps, out, residual
+    method<adapters, 8>("lora_adapters"),        // y, x, down, up, adapter, scaling, ranks, out
     method<append, 5>("cache_append"),           // k, v, k_cache, v_cache, slots
     {nullptr, nullptr, 0, nullptr}};
 

@@ -553,6 +553,57 @@ typedef struct {
 int block_norm(const block_norm_t* args, void* stream);
 
 /*
+ * lora_adapters — low-rank adapters of many requests beside a projection that they
+ * share: for every row m with adapter a = adapter[m],
+ *
+ *     out[m] = y[m] + scaling[a] * (x[m] @ down[a]^T) @ up[a]
+ *
+ *   x        16-bit  [rows, K]            the projection's input
+ *   y        16-bit  [rows, N]            its result
+ *   down     16-bit  [adapters, rank, K]  dense, one rank per row
+ *   up       16-bit  [adapters, rank, N]  dense, likewise
+ *   adapter  int32   [rows] on the device; outside 0 .. adapters - 1: none, out[m] = y[m]
+ *   scaling  float   [adapters] on the device, or NULL: 1
+ *   ranks    int32   [adapters] on the device, or NULL: rank for all. Rows of down and up
+ *                    from ranks[a] on are not used; values outside 0 .. rank are
+ *                    taken as the nearest of the two
+ *
+ * One 16-bit type (f16). Sums in float32; x @ down^T stays in float32 (its product
+ * with up in two 16-bit parts); one rounding, to out. Rows may lie in any
+ * order; rows of a request, or of requests with one adapter, beside each other share its reads.
+ *
+ * rows up to LORA_ADAPTERS_MAX_ROWS; rank 1 .. LORA_ADAPTERS_MAX_RANK; K a multiple
+ * of 8; K and N up to 2^30; any N. Row strides in elements, not negative, x's a multiple of 8; x and
+ * down 16-byte, y, up and out 2-byte, the others 4-byte aligned. out may be y itself
+ * with the same stride (in place); it may overlap nothing else, and its rows not each
+ * other (GEMM_W4A4_EINVAL). rows 0: nothing is enqueued.
+ *
+ * workspace: lora_adapters_workspace bytes, 16-byte aligned, that nothing else uses
+ * until the call's work on `stream` has finished. Fewer: GEMM_W4A4_ESCRATCH. Results do not
+ * depend on what it holds. Deterministic; no allocation, no synchronisation.
+ */
+#define LORA_ADAPTERS_MAX_RANK 128
+#define LORA_ADAPTERS_MAX_ROWS 4194240
+typedef struct {
+  const void* x;             /* 16-bit type, see f16 */
+  const void* y;
+  const void* down;
+  const void* up;
+  void* out;
+  const int32_t* adapter;
+  const float* scaling;
+  const int32_t* ranks;
+  int rows, K, N, adapters, rank;
+  int64_t x_stride, y_stride, out_stride;   /* of rows */
+  int f16;                   /* 0: bfloat16, 1: binary16 */
+  void* workspace;
+  int64_t workspace_bytes;
+} lora_adapters_t;
+int lora_adapters(const lora_adapters_t* args, void* stream);
+/* Workspace bytes of this call (sizes only; no pointer is read), or GEMM_W4A4_EINVAL (host only). */
+int64_t lora_adapters_workspace(const lora_adapters_t* args);
+
+/*
  * cache_append — keys and values of new tokens, k and v [tokens, heads,
  * head_dim], into a paged cache, k_cache and v_cache [pages, page_size, heads,
  * head_dim]: token t goes to place slots[t] % page_size of page slots[t] / page_size.

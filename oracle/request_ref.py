@@ -13,7 +13,7 @@ import numpy as np
 
 from .block_ref import half_spacing
 
-__all__ = ["block_norm_ref", "cache_append_ref"]
+__all__ = ["block_norm_ref", "cache_append_ref", "lora_adapters_ref"]
 
 # relative error of a float32 sum of a row: at most 64 additions in a lane and 12
 # across lanes and waves, each off by 2^-24 of the partial sum
@@ -73,3 +73,33 @@ def cache_append_ref(k, v, k_cache, v_cache, slots):
             kc[s // page, s % page] = k[t]
             vc[s // page, s % page] = v[t]
     return kc, vc
+
+
+def lora_adapters_ref(y, x, down, up, adapter, scaling=None, ranks=None, dtype="bf16"):
+    """y [rows, N], x [rows, K], down [A, R, K], up [A, R, N], adapter [rows] -> (out, bound).
+
+    The bound, with L = |x| |down|^T, T = scaling L |up| and K-term float32 sums in an order
+    of their own (products of 16-bit values are exact; a chain of at most K / 8 + 64
+    additions, each off by 2^-24 of at most L): low off by (K / 8 + 64) 2^-24 L; its two 16-bit
+    parts by 2^-17 (bf16: 2^-9 of 2^-9, and their products' rounding; f16 less), and,
+    f16 after scaling to 2^15, by 2^-25 2^-14 of the largest low of the row for each part of
+    it that is subnormal; the second sum by (R / 8 + 8) 2^-24 T."""
+    rows, K = x.shape
+    R = down.shape[1]
+    out, bound = y.copy(), np.zeros_like(y)
+    for m in range(rows):
+        a = int(adapter[m])
+        if not 0 <= a < down.shape[0]:
+            continue
+        r = R if ranks is None else min(max(int(ranks[a]), 0), R)
+        s = 1.0 if scaling is None else float(np.float32(scaling[a]))
+        d, w = down[a, :r], up[a, :r]
+        low = d @ x[m]
+        mag = np.abs(d) @ np.abs(x[m])
+        out[m] += s * (low @ w)
+        T = abs(s) * (mag @ np.abs(w))
+        top = abs(s) * (np.abs(low).max() if r else 0.0)
+        bound[m] = T * ((K / 8 + 64 + R / 8 + 8) * 2.0 ** -24) + abs(s) * (np.abs(low) @ np.abs(w)) * 2.0 ** -17 + \
+            (2.0 ** -38 * top * np.abs(w).sum(0) if dtype == "f16" else 0.0) + 2.0 ** -23 * (np.abs(y[m]) + T)
+    some = bound > 0
+    return out, np.where(some, bound + 0.5 * half_spacing(out, dtype) * (1 + 2.0 ** -6), 0.0)

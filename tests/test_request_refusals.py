@@ -94,6 +94,51 @@ def test_append_empty_and_null():
     assert w4._native.load().cache_append(None, None) == w4.EINVAL
 
 
+# ---------------------------------------------------------------- lora_adapters
+
+def adapt(**over):
+    a = dict(x=0x10000000, y=0x20000000, down=0x30000000, up=0x40000000, out=0x50000000, adapter=0x60000000, scaling=0x61000000,
+             ranks=0x62000000, rows=10, K=64, N=100, adapters=3, rank=16, x_stride=64, y_stride=100, out_stride=100, f16=0,
+             workspace=0x70000000, workspace_bytes=1 << 20)
+    a.update(over)
+    return w4.LoraAdaptersArgs(*a.values())
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(rows=-1), "EINVAL"), (dict(rows=w4.LORA_ADAPTERS_MAX_ROWS + 1), "EINVAL"), (dict(K=0), "EINVAL"), (dict(K=60), "EINVAL"),
+    (dict(N=0), "EINVAL"), (dict(N=(1 << 30) + 1), "EINVAL"), (dict(adapters=0), "EINVAL"), (dict(rank=0), "EINVAL"),
+    (dict(rank=129), "EINVAL"), (dict(f16=2), "EINVAL"), (dict(x_stride=-64), "EINVAL"), (dict(x_stride=68), "EINVAL"),
+    (dict(out_stride=99), "EINVAL"), (dict(out_stride=0), "EINVAL"), (dict(y_stride=1 << 61), "EINVAL"),
+    (dict(adapters=2**31 - 1, rank=128, K=1 << 30), "EINVAL"), (dict(x=0), "EINVAL"), (dict(y=0), "EINVAL"), (dict(down=0), "EINVAL"),
+    (dict(up=0), "EINVAL"), (dict(out=0), "EINVAL"), (dict(adapter=0), "EINVAL"), (dict(x=0x10000008), "EALIGN"),
+    (dict(down=0x30000002), "EALIGN"), (dict(up=0x40000001), "EALIGN"), (dict(y=0x20000001), "EALIGN"), (dict(adapter=0x60000002), "EALIGN"),
+    (dict(scaling=0x61000001), "EALIGN"), (dict(ranks=0x62000002), "EALIGN"), (dict(workspace=0), "ESCRATCH"),
+    (dict(workspace_bytes=64), "ESCRATCH"), (dict(workspace=0x70000008), "EALIGN"), (dict(out=0x20000002), "EOVERLAP"),
+    (dict(out=0x20000000, out_stride=104), "EOVERLAP"), (dict(out=0x10000000), "EOVERLAP"), (dict(out=0x30000100), "EOVERLAP"),
+    (dict(up=0x50000000), "EOVERLAP"), (dict(adapter=0x50000010), "EOVERLAP"), (dict(workspace=0x10000000), "EOVERLAP"),
+    (dict(workspace=0x50000000), "EOVERLAP"), (dict(scaling=0x70000000), "EOVERLAP")])
+def test_adapters_refuse(over, code):
+    assert w4.lora_adapters_raw(adapt(**over), 0) == getattr(w4, code)
+
+
+@pytest.mark.parametrize("over", [
+    dict(), dict(scaling=0, ranks=0), dict(out=0x20000000), dict(x_stride=0, y_stride=0), dict(rows=1, x_stride=3, out_stride=0),
+    dict(y=0x20000002, up=0x40000002, out=0x50000002)])
+def test_adapters_accept(over):
+    assert w4.lora_adapters_raw(adapt(**over), 0) in REACHED
+
+
+def test_adapters_empty_null_and_workspace():
+    assert w4.lora_adapters_raw(adapt(rows=0, x=0, workspace=0), 0) == w4.OK
+    lib = w4._native.load()
+    assert lib.lora_adapters(None, None) == w4.EINVAL and lib.lora_adapters_workspace(None) == w4.EINVAL
+    need = w4.lora_adapters_workspace
+    assert need(adapt(K=60)) == w4.EINVAL and need(adapt(rows=0)) == 0
+    assert need(adapt(rows=1000, rank=17)) % (1000 * 32 * 4) == 0
+    top = need(adapt(rows=w4.LORA_ADAPTERS_MAX_ROWS, rank=128, N=1 << 30, K=1 << 30))
+    assert top >= w4.LORA_ADAPTERS_MAX_ROWS * 128 * 4
+
+
 # ---------------------------------------------------------------- the Python checks
 
 def test_python_checks():
@@ -106,7 +151,7 @@ def test_python_checks():
         w4.cache_append(*(z(1, 1, 8, dtype=bf) for _ in range(4)), z(1, dtype=torch.int64))
 
 
-STRUCTURES = {"block_norm_t": "BlockNormArgs", "cache_append_t": "CacheAppendArgs"}
+STRUCTURES = {"block_norm_t": "BlockNormArgs", "lora_adapters_t": "LoraAdaptersArgs", "cache_append_t": "CacheAppendArgs"}
 
 
 def test_structures_match_the_header(tmp_path):
