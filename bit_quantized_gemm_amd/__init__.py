@@ -13,7 +13,9 @@ MXFP4 producer), gemm_mxfp4_few (the MXFP4 layer for few rows), rotary_axes
 (rotary positions over several axes) and cross_attention (attention to keys of
 another length). For many requests at once: block_norm (norms with gate and
 residual), lora_adapters (each request's own low-rank adapter beside a shared
-projection) and cache_append (keys and values into a paged cache).
+projection), packed_attention (causal attention over packed prompts),
+cache_append (keys and values into a paged cache) and paged_attention (the
+newest tokens over that cache).
 
 PyTorch supplies device memory and the stream; every step of the operator runs
 in the library's HIP kernels. If the library is missing the calls raise.
@@ -25,9 +27,10 @@ from ._native import (ATTENTION_MAX_HEAD_DIM, FEW_MAX_M, ROTARY_MAX_AXES, ROTARY
                       AttentionArgs, RotaryArgs,
                       cross_attention_raw, cross_attention_workspace, gemm_mxfp4_few_raw, quantize_mxfp4_raw,
                       quantize_mxfp4_workspace, rotary_axes_raw)
-from ._native import (BLOCK_NORM_MAX_WIDTH, LORA_ADAPTERS_MAX_RANK, LORA_ADAPTERS_MAX_ROWS,
-                      BlockNormArgs, CacheAppendArgs, LoraAdaptersArgs,
-                      block_norm_raw, cache_append_raw, lora_adapters_raw, lora_adapters_workspace)
+from ._native import (BLOCK_NORM_MAX_WIDTH, LORA_ADAPTERS_MAX_RANK, LORA_ADAPTERS_MAX_ROWS, PACKED_ATTENTION_MAX_SEQS,
+                      PAGED_ATTENTION_PAGE_MULTIPLE, BlockNormArgs, CacheAppendArgs, LoraAdaptersArgs, PackedAttentionArgs,
+                      PagedAttentionArgs, block_norm_raw, cache_append_raw, lora_adapters_raw, lora_adapters_workspace,
+                      packed_attention_raw, paged_attention_raw, paged_attention_workspace)
 from ._native import (EALIGN, EDEVICE, EINVAL, ENOMEM, ESCRATCH, ELAUNCH, EOVERLAP, FORMATS, MAX_R, OK, QUANTIZE_MAX_R,
                       quantize_noalloc_raw, quantize_plan, quantize_raw,
                       gemm_mxfp4_f16_raw, gemm_mxfp4_raw, gemm_w4a4_f16_raw, gemm_w4a4_raw,
@@ -39,7 +42,9 @@ __all__ = ["quantize_mxfp4_act", "gemm_mxfp4_few", "rotary_axes", "cross_attenti
            "ROTARY_MAX_HEAD_DIM", "ATTENTION_MAX_HEAD_DIM",
            "block_norm", "cache_append", "block_norm_raw", "cache_append_raw", "BlockNormArgs", "CacheAppendArgs",
            "BLOCK_NORM_MAX_WIDTH", "lora_adapters", "lora_adapters_raw", "lora_adapters_workspace", "LoraAdaptersArgs",
-           "LORA_ADAPTERS_MAX_RANK", "LORA_ADAPTERS_MAX_ROWS",
+           "LORA_ADAPTERS_MAX_RANK", "LORA_ADAPTERS_MAX_ROWS", "packed_attention", "packed_attention_raw", "PackedAttentionArgs",
+           "PACKED_ATTENTION_MAX_SEQS", "paged_attention", "paged_attention_raw", "paged_attention_workspace", "PagedAttentionArgs",
+           "PAGED_ATTENTION_PAGE_MULTIPLE",
            "gemm_w4a4", "gemm_mxfp4", "quantize_w4a4_act", "quantize_raw", "quantize_noalloc_raw", "quantize_plan", "QUANTIZE_MAX_R", "gemm_w4a4_raw", "gemm_w4a4_f16_raw", "gemm_mxfp4_raw",
            "gemm_mxfp4_f16_raw", "run_raw", "plan", "plan_variant", "variants", "strerror", "library_path", "GemmError", "OK",
            "EINVAL", "EALIGN", "ELAUNCH", "EOVERLAP", "EDEVICE", "ENOMEM", "ESCRATCH", "MAX_R", "FORMATS"]
@@ -324,3 +329,35 @@ def cross_attention(q, k, v, kv_lens=None, scale=None, return_lse=False, out=Non
     [batch, q_heads, q_len] (-inf for rows without keys). No gradient is recorded.
     """
     return _run("cross_attention", stream, q, k, v, kv_lens, scale, return_lse, out)
+
+
+def packed_attention(q, k, v, starts, causal=True, scale=None, return_lse=False, out=None, stream=None):
+    """Enqueue attention within sequences packed one after the other on `stream`.
+
+    q bfloat16 or float16 [tokens, q_heads, head_dim]; k, v [tokens, kv_heads, head_dim]
+    of q's type, q_heads a multiple of kv_heads (neighbouring query heads share a key
+    head); any strides that are multiples of 8 with a dense last dimension; head_dim a
+    multiple of 8 up to ATTENTION_MAX_HEAD_DIM. starts int32 [sequences + 1] on the device: sequence
+    s is the tokens starts[s] .. starts[s + 1] - 1 (may be none). A token sees its
+    sequence's tokens, when causal those up to itself. scale: default head_dim ** -0.5. Returns out [tokens,
+    q_heads, head_dim] (allocated dense when None), and with return_lse also the
+    float32 log-sum-exp [q_heads, tokens]; tokens in no sequence (padding behind the last) keep what an out that was
+    given holds, and have no defined value in a result that was allocated. No gradient is recorded.
+    """
+    return _run("packed_attention", stream, q, k, v, starts, causal, scale, return_lse, out)
+
+
+def paged_attention(q, k_cache, v_cache, table, lens, scale=None, return_lse=False, out=None, stream=None):
+    """Enqueue attention of the newest tokens of each sequence over a paged cache on `stream`.
+
+    q bfloat16 or float16 [batch, q_len, q_heads, head_dim], the newest q_len tokens of each sequence (1: one
+    step of decoding); k_cache, v_cache [pages, page_size, kv_heads, head_dim] of q's type, which hold
+    their keys and values already (cache_append); page_size a multiple of
+    PAGED_ATTENTION_PAGE_MULTIPLE; strides and heads as for cross_attention. table int32
+    [batch, width] on the device: page table[b, i] holds the keys i * page_size .. of sequence b (no page in
+    the cache: its keys are left out); lens int32 [batch] on the device: keys of each sequence, the new ones among them. New token
+    i sees the keys up to lens[b] - q_len + i; rows that see none give 0. scale: default head_dim ** -0.5. Returns out
+    [batch, q_len, q_heads, head_dim] (allocated dense when None), and with return_lse also the float32
+    log-sum-exp [batch, q_heads, q_len] (-inf for rows that see no key). No gradient is recorded.
+    """
+    return _run("paged_attention", stream, q, k_cache, v_cache, table, lens, scale, return_lse, out)

@@ -89,6 +89,23 @@ class LoraAdaptersArgs(ctypes.Structure):
                [("f16", ctypes.c_int), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
+class PackedAttentionArgs(ctypes.Structure):
+    """packed_attention_t."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k", "v", "out", "lse", "starts")] + \
+               [(f, ctypes.c_int) for f in ("tokens", "seqs", "q_heads", "kv_heads", "head_dim")] + \
+               [(f, ctypes.c_int64 * 2) for f in ("q_stride", "k_stride", "v_stride", "out_stride")] + \
+               [("scale", ctypes.c_float), ("causal", ctypes.c_int), ("f16", ctypes.c_int)]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    """paged_attention_t."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k_cache", "v_cache", "out", "lse", "table", "lens")] + \
+               [(f, ctypes.c_int) for f in ("batch", "q_len", "q_heads", "kv_heads", "head_dim", "pages", "page_size", "table_width")] + \
+               [(f, ctypes.c_int64 * 3) for f in ("q_stride", "k_stride", "v_stride", "out_stride")] + \
+               [("table_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("f16", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
 class Plan(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int) for f in _PLAN_FIELDS]
 
@@ -161,11 +178,12 @@ def load() -> ctypes.CDLL:
         lib.cross_attention.restype = i
         lib.cross_attention_workspace.argtypes = [vp]
         lib.cross_attention_workspace.restype = i64
-        for name in ("block_norm", "cache_append", "lora_adapters"):
+        for name in ("block_norm", "cache_append", "lora_adapters", "packed_attention", "paged_attention"):
             getattr(lib, name).argtypes = [vp, vp]
             getattr(lib, name).restype = i
-        lib.lora_adapters_workspace.argtypes = [vp]
-        lib.lora_adapters_workspace.restype = i64
+        for name in ("lora_adapters_workspace", "paged_attention_workspace"):
+            getattr(lib, name).argtypes = [vp]
+            getattr(lib, name).restype = i64
         lib.gemm_w4a4_strerror.argtypes = [i]
         lib.gemm_w4a4_strerror.restype = ctypes.c_char_p
         _lib = lib
@@ -243,6 +261,8 @@ ATTENTION_MAX_HEAD_DIM = 128
 BLOCK_NORM_MAX_WIDTH = 16384
 LORA_ADAPTERS_MAX_RANK = 128
 LORA_ADAPTERS_MAX_ROWS = 4194240
+PACKED_ATTENTION_MAX_SEQS = 1 << 20
+PAGED_ATTENTION_PAGE_MULTIPLE = 16
 
 
 def quantize_mxfp4_raw(f16, x, lora_down, act, ascales, lora_act_in, M, K, R, workspace, workspace_bytes,
@@ -300,6 +320,21 @@ def lora_adapters_raw(args: "LoraAdaptersArgs", stream) -> int:
 def lora_adapters_workspace(args: "LoraAdaptersArgs") -> int:
     """Workspace bytes of a lora_adapters call, or a negative code (host only)."""
     return load().lora_adapters_workspace(ctypes.byref(args))
+
+
+def packed_attention_raw(args: "PackedAttentionArgs", stream) -> int:
+    """Direct call of packed_attention; returns its code."""
+    return load().packed_attention(ctypes.byref(args), stream)
+
+
+def paged_attention_raw(args: "PagedAttentionArgs", stream) -> int:
+    """Direct call of paged_attention; returns its code."""
+    return load().paged_attention(ctypes.byref(args), stream)
+
+
+def paged_attention_workspace(args: "PagedAttentionArgs") -> int:
+    """Workspace bytes of a paged_attention call, or a negative code (host only)."""
+    return load().paged_attention_workspace(ctypes.byref(args))
 
 
 def quantize_plan(M: int, K: int, R: int) -> dict:

@@ -39,7 +39,7 @@ PROBES_LIB_PATH = os.path.join(PKG_DIR, "libw4a4_probes.so")
 LIBS = {
     LIB_PATH: (("gemm_w4a4.hip", "gemm_mxfp4.hip", "w4a4_producer.hip", "mxfp4_producer.hip",
                 "mxfp4_few.hip", "rotary.hip", "attention.hip", "block_norm.hip", "cache_append.hip",
-                "lora_adapters.hip"), True),
+                "lora_adapters.hip", "packed_attention.hip", "paged_attention.hip"), True),
     PROBES_LIB_PATH: (("mfma_peak.hip", "route_probe.hip"), False),
 }
 BINDING_PATH = os.path.join(PKG_DIR, "_torch_binding.so")

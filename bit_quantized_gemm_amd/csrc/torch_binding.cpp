@@ -578,6 +578,140 @@ PyObject* append(PyObject* const* a) {
   return r;
 }
 
+float scale_of(PyObject* o, int head_dim) {
+  const float s = o == Py_None ? float(1.0 / std::sqrt(double(head_dim))) : float(PyFloat_AsDouble(o));
+  if (PyErr_Occurred()) throw Raised{};
+  return s;
+}
+
+// Strides of all dimensions but the last, which is dense.
+template <int N>
+void but_last(int64_t (&to)[N], const Tensor& t, const char* name) {
+  if (t.size(N) > 1 && t.stride(N) != 1) raise(PyExc_ValueError, std::string("the last dimension of ") + name + " must be dense");
+  for (int i = 0; i < N; ++i) to[i] = t.stride(i);
+}
+
+PyObject* with_lse(const Tensor& out, const Tensor& lse) {
+  if (!lse.defined()) return wrap(out);
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, wrap(out));
+  PyTuple_SET_ITEM(r, 1, wrap(lse));
+  return r;
+}
+
+PyObject* packed(PyObject* const* a) {
+  const Tensor& q = tensor(a[0], "q");
+  const Tensor& k = tensor(a[1], "k");
+  const Tensor& v = tensor(a[2], "v");
+  const Tensor& starts = tensor(a[3], "starts");
+  packed_attention_t c{};
+  c.f16 = half_of(q, "q");
+  if (q.dim() != 3 || k.dim() != 3) raise(PyExc_ValueError, "q, k and v must be [tokens, heads, head_dim]");
+  const c10::Device device = q.device();
+  c.tokens = dim_of(q.size(0), "q");
+  c.q_heads = dim_of(q.size(1), "q");
+  c.head_dim = dim_of(q.size(2), "q");
+  c.kv_heads = dim_of(k.size(1), "k");
+  const int64_t keys[3] = {c.tokens, c.kv_heads, c.head_dim};
+  same_kind(k, "k", q, keys);
+  same_kind(v, "v", q, keys);
+  if (starts.dim() != 1 || starts.size(0) < 1) raise(PyExc_ValueError, "starts must be [sequences + 1]");
+  want(starts, "starts", at::kInt, {starts.size(0)}, device.index());
+  c.seqs = dim_of(starts.size(0) - 1, "starts");
+  c.causal = truth(a[4]);
+  c.scale = scale_of(a[5], c.head_dim);
+  Tensor out;
+  if (a[7] == Py_None) {
+    out = empty(q.sizes(), q.scalar_type(), device);
+  } else {
+    out = tensor(a[7], "out");
+    same_kind(out, "out", q, q.sizes());
+  }
+  Tensor lse;
+  if (truth(a[6])) {
+    lse = empty({c.q_heads, c.tokens}, at::kFloat, device);
+    c.lse = ptr<float>(lse);
+  }
+  but_last(c.q_stride, q, "q");
+  but_last(c.k_stride, k, "k");
+  but_last(c.v_stride, v, "v");
+  but_last(c.out_stride, out, "out");
+  c.q = q.data_ptr();
+  c.k = k.data_ptr();
+  c.v = v.data_ptr();
+  c.out = out.data_ptr();
+  c.starts = ptr<int32_t>(starts);
+  const OnDevice on(device);
+  const int rc = packed_attention(&c, on.stream);
+  if (rc != GEMM_W4A4_OK) return PyLong_FromLong(rc);
+  written(a[7]);
+  return with_lse(out, lse);
+}
+
+PyObject* paged(PyObject* const* a) {
+  const Tensor& q = tensor(a[0], "q");
+  const Tensor& kc = tensor(a[1], "k_cache");
+  const Tensor& vc = tensor(a[2], "v_cache");
+  const Tensor& table = tensor(a[3], "table");
+  const Tensor& lens = tensor(a[4], "lens");
+  paged_attention_t c{};
+  c.f16 = half_of(q, "q");
+  if (q.dim() != 4) raise(PyExc_ValueError, "q must be [batch, q_len, q_heads, head_dim]");
+  caches(kc, vc, q);
+  if (kc.size(3) != q.size(3)) raise(PyExc_ValueError, "k_cache has heads of " + std::to_string(kc.size(3)) + ", q of " + std::to_string(q.size(3)));
+  const c10::Device device = q.device();
+  c.batch = dim_of(q.size(0), "q");
+  c.q_len = dim_of(q.size(1), "q");
+  c.q_heads = dim_of(q.size(2), "q");
+  c.head_dim = dim_of(q.size(3), "q");
+  c.pages = dim_of(kc.size(0), "k_cache");
+  c.page_size = dim_of(kc.size(1), "k_cache");
+  c.kv_heads = dim_of(kc.size(2), "k_cache");
+  if (table.scalar_type() != at::kInt) raise(PyExc_TypeError, std::string("table must be Int, got ") + type_text(table.scalar_type()));
+  if (table.dim() != 2 || table.size(0) != c.batch) raise(PyExc_ValueError, "table must be [batch, width], got " + shape_text(table.sizes()));
+  if (table.device() != device) raise(PyExc_ValueError, "table is on " + table.device().str() + ", expected " + device.str());
+  if (table.size(1) > 1 && table.stride(1) != 1) raise(PyExc_ValueError, "the last dimension of table must be dense");
+  c.table_width = dim_of(table.size(1), "table");
+  c.table_stride = table.stride(0);
+  want(lens, "lens", at::kInt, {c.batch}, device.index());
+  c.scale = scale_of(a[5], c.head_dim);
+  Tensor out;
+  if (a[7] == Py_None) {
+    out = empty(q.sizes(), q.scalar_type(), device);
+  } else {
+    out = tensor(a[7], "out");
+    same_kind(out, "out", q, q.sizes());
+  }
+  Tensor lse;
+  if (truth(a[6])) {
+    lse = empty({c.batch, c.q_heads, c.q_len}, at::kFloat, device);
+    c.lse = ptr<float>(lse);
+  }
+  but_last(c.q_stride, q, "q");
+  but_last(c.k_stride, kc, "k_cache");
+  but_last(c.v_stride, vc, "v_cache");
+  but_last(c.out_stride, out, "out");
+  c.q = q.data_ptr();
+  c.k_cache = kc.data_ptr();
+  c.v_cache = vc.data_ptr();
+  c.out = out.data_ptr();
+  c.table = ptr<int32_t>(table);
+  c.lens = ptr<int32_t>(lens);
+  const OnDevice on(device);
+  c.workspace_bytes = paged_attention_workspace(&c);
+  if (c.workspace_bytes < 0) return PyLong_FromLong(long(c.workspace_bytes));
+  Tensor ws;
+  if (c.workspace_bytes > 0) {
+    ws = empty({c.workspace_bytes}, at::kByte, device);
+    c.workspace = ws.data_ptr();
+  }
+  const int rc = paged_attention(&c, on.stream);
+  if (rc != GEMM_W4A4_OK) return PyLong_FromLong(rc);
+  written(a[7]);
+  return with_lse(out, lse);
+}
+
 // ---------------------------------------------------------------- the module
 
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -609,6 +743,8 @@ PyMethodDef g_methods[] = {
     method<norm, 14>("block_norm"),              // x .. shift, eps, out, residual
     method<adapters, 8>("lora_adapters"),        // y, x, down, up, adapter, scaling, ranks, out
     method<append, 5>("cache_append"),           // k, v, k_cache, v_cache, slots
+    method<packed, 8>("packed_attention"),       // q, k, v, starts, causal, scale, return_lse, out
+    method<paged, 8>("paged_attention"),         // q, k_cache, v_cache, table, lens, scale, return_lse, out
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

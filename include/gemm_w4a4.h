@@ -632,6 +632,101 @@ typedef struct {
 } cache_append_t;
 int cache_append(const cache_append_t* args, void* stream);
 
+/*
+ * packed_attention — attention within sequences of different lengths that lie one
+ * after the other in q [tokens, q_heads, head_dim] and k, v [tokens, kv_heads,
+ * head_dim]: sequence s is the tokens starts[s] .. starts[s + 1] - 1,
+ *
+ *     out[i, h] = sum_j softmax_j(scale * q[i,h] . k[j,g]) v[j,g],   g = h / (q_heads / kv_heads),
+ *
+ * over the tokens j of i's sequence, with causal those up to i itself.
+ *
+ *   starts    int32 [seqs + 1] on the device, rising (equal: an empty sequence). Values outside
+ *             0 .. tokens are taken as the nearest of the two, a sequence that ends before it
+ *             starts as empty; what sequences that overlap give is not defined.
+ *   lse       float [q_heads, tokens], written when not NULL: the natural log of the sum
+ *             of exp(scale * q . k)
+ *
+ * Rows of out and lse in no sequence (before the first start, from the last on) stay as they
+ * are. What k and v hold for tokens that a row does not see does not matter to it, infinities
+ * and NaN included. Arithmetic as for cross_attention.
+ *
+ * scale, head_dim, heads, strides (token, head) and alignment as for cross_attention, v's
+ * token stride at least head_dim; tokens * q_heads at most 2^31 - CROSS_ATTENTION_PAST_END; seqs up to
+ * PACKED_ATTENTION_MAX_SEQS; kv_heads below 2^20. tokens, seqs or q_heads 0: nothing is
+ * enqueued. One launch, no workspace; deterministic.
+ */
+#define PACKED_ATTENTION_MAX_SEQS (1 << 20)
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  const int32_t* starts;
+  int tokens, seqs, q_heads, kv_heads, head_dim;
+  int64_t q_stride[2];       /* token, head */
+  int64_t k_stride[2];
+  int64_t v_stride[2];
+  int64_t out_stride[2];
+  float scale;
+  int causal;
+  int f16;                   /* 0: bfloat16, 1: binary16 */
+} packed_attention_t;
+int packed_attention(const packed_attention_t* args, void* stream);
+
+/*
+ * paged_attention — attention of the newest q_len tokens of each sequence, q [batch, q_len,
+ * q_heads, head_dim], over its keys and values in a paged cache, k_cache and v_cache
+ * [pages, page_size, kv_heads, head_dim] (cache_append):
+ *
+ *   table     int32 [batch, table_width] on the device: page table[b][i] holds the keys
+ *             i * page_size .. of sequence b. Entries past its last key are not used.
+ *             An entry outside 0 .. pages - 1 is no page: its keys are left out.
+ *   lens      int32 [batch] on the device: keys of each sequence, the new tokens' own among
+ *             them (append them first). Values outside 0 .. table_width * page_size
+ *             are taken as the nearest of the two.
+ *
+ * New token i of sequence b sees the keys j <= lens[b] - q_len + i; a row that sees none gives out 0
+ * and lse -inf. lse float [batch, q_heads, q_len], written when not NULL. Keys from
+ * lens[b] on are never read; what keys and values hold that a row does not see does not matter to it.
+ * Arithmetic as for cross_attention.
+ *
+ * page_size a multiple of PAGED_ATTENTION_PAGE_MULTIPLE; table_width * page_size and q_len below
+ * 2^30 - CROSS_ATTENTION_PAST_END; scale, head_dim, heads, strides (q and out: batch, token, head; caches: page,
+ * token, head; table: batch), alignment and limits of rows as for cross_attention, v_cache's token
+ * stride at least head_dim. Made for few new tokens: every 32 rows (token, query head of
+ * a key head) read the keys anew. batch, q_len or q_heads 0: nothing is enqueued; pages or
+ * table_width 0: no keys, caches and table may be NULL.
+ *
+ * workspace: paged_attention_workspace bytes, 16-byte aligned, that nothing else uses until the call's
+ * work on `stream` has finished (0: NULL is fine). Fewer: GEMM_W4A4_ESCRATCH. Deterministic; no
+ * allocation, no synchronisation.
+ */
+#define PAGED_ATTENTION_PAGE_MULTIPLE 16
+typedef struct {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  void* out;
+  float* lse;
+  const int32_t* table;
+  const int32_t* lens;
+  int batch, q_len, q_heads, kv_heads, head_dim, pages, page_size, table_width;
+  int64_t q_stride[3];       /* batch, token, head */
+  int64_t k_stride[3];       /* page, token, head */
+  int64_t v_stride[3];
+  int64_t out_stride[3];
+  int64_t table_stride;
+  float scale;
+  int f16;                   /* 0: bfloat16, 1: binary16 */
+  void* workspace;
+  int64_t workspace_bytes;
+} paged_attention_t;
+int paged_attention(const paged_attention_t* args, void* stream);
+/* Workspace bytes of this call (sizes only; no pointer is read), or GEMM_W4A4_EINVAL (host only). */
+int64_t paged_attention_workspace(const paged_attention_t* args);
+
 /* Static string for a return code (never NULL). */
 const char* gemm_w4a4_strerror(int code);
 

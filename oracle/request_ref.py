@@ -13,7 +13,7 @@ import numpy as np
 
 from .block_ref import half_spacing
 
-__all__ = ["block_norm_ref", "cache_append_ref", "lora_adapters_ref"]
+__all__ = ["block_norm_ref", "cache_append_ref", "lora_adapters_ref", "packed_attention_ref", "paged_attention_ref"]
 
 # relative error of a float32 sum of a row: at most 64 additions in a lane and 12
 # across lanes and waves, each off by 2^-24 of the partial sum
@@ -103,3 +103,77 @@ def lora_adapters_ref(y, x, down, up, adapter, scaling=None, ranks=None, dtype="
             (2.0 ** -38 * top * np.abs(w).sum(0) if dtype == "f16" else 0.0) + 2.0 ** -23 * (np.abs(y[m]) + T)
     some = bound > 0
     return out, np.where(some, bound + 0.5 * half_spacing(out, dtype) * (1 + 2.0 ** -6), 0.0)
+
+
+def _attend(q, k, v, sees, scale, dtype):
+    """One head: q [n, D], k, v [m, D], sees [n]: row i sees the first sees[i] keys -> out, lse and their bounds.
+
+    The bounds are those of attention_ref in block_ref.py: weights off by the unit
+    roundoff of the 16-bit type and by twice the float32 error of their scores."""
+    n, D = q.shape
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    out, bound = np.zeros((n, D)), np.zeros((n, D))
+    lse, lse_bound = np.full(n, -np.inf), np.zeros(n)
+    m = int(max(sees.max(initial=0), 0))
+    live = np.arange(m)[None, :] < sees[:, None]
+    rows = live.any(1)
+    if not rows.any():
+        return out, lse, bound, lse_bound
+    q, live = q[rows], live[rows]
+    k, v = k[:m], v[:m]
+    s = np.where(live, scale * (q @ k.T), -np.inf)
+    top = s.max(axis=1, keepdims=True)
+    p = np.exp(s - top)
+    total = p.sum(axis=1, keepdims=True)
+    o = p @ v / total
+    ds = (D + 8) * 2.0 ** -24 * np.where(live, scale * (np.abs(q) @ np.abs(k).T), 0.0).max(axis=1, keepdims=True) \
+        + 2.0 ** -22 * np.abs(np.where(live, s, 0.0)).max(axis=1, keepdims=True)
+    T = p @ np.abs(v) / total
+    tiny = 2.0 ** -25 * (live @ np.abs(v)) if dtype == "f16" else 0.0
+    out[rows] = o
+    lse[rows] = (top + np.log(total))[:, 0]
+    bound[rows] = 2 * T * (u + 2 * ds + 2.0 ** -20) + 0.5 * half_spacing(o, dtype) * (1 + 2.0 ** -6) + tiny
+    lse_bound[rows] = (2 * ds)[:, 0] + 2.0 ** -20 * (1 + np.abs(lse[rows]))
+    return out, lse, bound, lse_bound
+
+
+def packed_attention_ref(q, k, v, starts, causal=True, scale=None, dtype="bf16"):
+    """q [T, HQ, D], k, v [T, HKV, D] -> (out, lse [HQ, T], their bounds, whether a token is in a sequence [T])."""
+    T, HQ, D = q.shape
+    group = HQ // k.shape[1]
+    scale = D ** -0.5 if scale is None else scale
+    out, bound = np.zeros((T, HQ, D)), np.zeros((T, HQ, D))
+    lse, lse_bound = np.full((HQ, T), -np.inf), np.zeros((HQ, T))
+    inside = np.zeros(T, dtype=bool)
+    at = np.clip(np.asarray(starts, dtype=np.int64), 0, T)
+    for a, b in zip(at[:-1], at[1:]):
+        n = b - a
+        if n <= 0:
+            continue
+        inside[a:b] = True
+        sees = np.arange(1, n + 1) if causal else np.full(n, n)
+        for h in range(HQ):
+            g = h // group
+            out[a:b, h], lse[h, a:b], bound[a:b, h], lse_bound[h, a:b] = _attend(q[a:b, h], k[a:b, g], v[a:b, g], sees, scale, dtype)
+    return out, lse, bound, lse_bound, inside
+
+
+def paged_attention_ref(q, k_cache, v_cache, table, lens, scale=None, dtype="bf16"):
+    """q [B, Q, HQ, D], caches [pages, page, HKV, D] -> (out, lse [B, HQ, Q], their bounds)."""
+    B, Q, HQ, D = q.shape
+    pages, page, HKV, _ = k_cache.shape
+    group = HQ // HKV
+    scale = D ** -0.5 if scale is None else scale
+    out, bound = np.zeros(q.shape), np.zeros(q.shape)
+    lse, lse_bound = np.full((B, HQ, Q), -np.inf), np.zeros((B, HQ, Q))
+    for b in range(B):
+        n = min(max(int(lens[b]), 0), table.shape[1] * page)
+        keys = np.array([(table[b][j // page], j % page) for j in range(n)], dtype=np.int64).reshape(-1, 2)
+        there = (keys[:, 0] >= 0) & (keys[:, 0] < pages)
+        # keys of a page that is none are left out: of those that are, row i sees so many
+        sees = np.array([int(there[:max(0, n - Q + 1 + i)].sum()) for i in range(Q)])
+        keys = keys[there]
+        for h in range(HQ):
+            k, v = (c[keys[:, 0], keys[:, 1], h // group] for c in (k_cache, v_cache))
+            out[b, :, h], lse[b, h], bound[b, :, h], lse_bound[b, h] = _attend(q[b, :, h], k, v, sees, scale, dtype)
+    return out, lse, bound, lse_bound

@@ -18,7 +18,8 @@ MADE_UP_ADDRESSES = {
     "test_abi.py": {"test_null_lora_allowed_without_rank_all_entries", "test_null_lora_allowed_without_rank",
                     "test_quantize_rank_zero_needs_no_lora_pointers"},
     "test_block_refusals.py": {"test_quantize_accepts", "test_few_accepts", "test_rotary_accepts", "test_attention_accepts"},
-    "test_request_refusals.py": {"test_norm_accepts", "test_append_accepts", "test_adapters_accept"},
+    "test_request_refusals.py": {"test_norm_accepts", "test_append_accepts", "test_adapters_accept", "test_packed_accepts",
+                                 "test_paged_accepts"},
 }
 
 

@@ -139,6 +139,101 @@ def test_adapters_empty_null_and_workspace():
     assert top >= w4.LORA_ADAPTERS_MAX_ROWS * 128 * 4
 
 
+# ---------------------------------------------------------------- packed_attention
+
+def packed(**over):
+    a = dict(q=0x10000000, k=0x20000000, v=0x30000000, out=0x40000000, lse=0, starts=0x50000000, tokens=100, seqs=3, q_heads=4, kv_heads=2,
+             head_dim=64, q_stride=(256, 64), k_stride=(128, 64), v_stride=(128, 64), out_stride=(256, 64), scale=0.125, causal=1, f16=0)
+    a.update(over)
+    return w4.packed_attention_raw(w4.PackedAttentionArgs(*a.values()), 0)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(tokens=-1), "EINVAL"), (dict(seqs=-1), "EINVAL"), (dict(seqs=(1 << 20) + 1), "EINVAL"), (dict(q_heads=-4), "EINVAL"),
+    (dict(kv_heads=0), "EINVAL"), (dict(q_heads=5), "EINVAL"), (dict(head_dim=0), "EINVAL"), (dict(head_dim=60), "EINVAL"),
+    (dict(head_dim=136), "EINVAL"), (dict(scale=0.0), "EINVAL"), (dict(scale=float("nan")), "EINVAL"), (dict(causal=2), "EINVAL"),
+    (dict(f16=-1), "EINVAL"), (dict(tokens=1 << 29), "EINVAL"), (dict(q_heads=1 << 20, kv_heads=1 << 20), "EINVAL"),
+    (dict(tokens=2**31 - 1024, q_heads=1, kv_heads=1 << 20), "EINVAL"), (dict(q_stride=(-256, 64)), "EINVAL"), (dict(q_stride=(260, 64)), "EINVAL"),
+    (dict(k_stride=(1 << 23, 64)), "EINVAL"), (dict(v_stride=(56, 64)), "EINVAL"), (dict(v_stride=(0, 64)), "EINVAL"),
+    (dict(out_stride=(256, 0)), "EINVAL"), (dict(out_stride=(192, 64)), "EINVAL"), (dict(q=0), "EINVAL"), (dict(v=0), "EINVAL"),
+    (dict(out=0), "EINVAL"), (dict(starts=0), "EINVAL"), (dict(q=0x10000008), "EALIGN"), (dict(k=0x20000002), "EALIGN"),
+    (dict(starts=0x50000002), "EALIGN"), (dict(lse=0x60000001), "EALIGN"), (dict(out=0x10000000), "EOVERLAP"), (dict(out=0x30000010), "EOVERLAP"),
+    (dict(lse=0x40000100), "EOVERLAP"), (dict(starts=0x40000100), "EOVERLAP"), (dict(lse=0x20000000), "EOVERLAP")])
+def test_packed_refuses(over, code):
+    assert packed(**over) == getattr(w4, code)
+
+
+@pytest.mark.parametrize("over", [
+    dict(), dict(causal=0, lse=0x60000000), dict(k=0x30000000), dict(k_stride=(0, 0), v_stride=(64, 0)), dict(tokens=1, v_stride=(8, 64)),
+    dict(seqs=1 << 20)])
+def test_packed_accepts(over):
+    assert packed(**over) in REACHED
+
+
+def test_packed_empty_and_null():
+    assert packed(tokens=0, q=0) == w4.OK and packed(seqs=0, starts=0) == w4.OK and packed(q_heads=0) == w4.OK
+    assert w4._native.load().packed_attention(None, None) == w4.EINVAL
+
+
+# ---------------------------------------------------------------- paged_attention
+
+def paged(**over):
+    a = dict(q=0x10000000, k_cache=0x20000000, v_cache=0x30000000, out=0x40000000, lse=0, table=0x50000000, lens=0x51000000, batch=2, q_len=1,
+             q_heads=4, kv_heads=2, head_dim=64, pages=9, page_size=16, table_width=4, q_stride=(256, 256, 64), k_stride=(2048, 128, 64),
+             v_stride=(2048, 128, 64), out_stride=(256, 256, 64), table_stride=4, scale=0.125, f16=0, workspace=0, workspace_bytes=0)
+    a.update(over)
+    return w4.PagedAttentionArgs(*a.values())
+
+
+CUT = dict(table_width=400)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(batch=-1), "EINVAL"), (dict(q_len=-1), "EINVAL"), (dict(q_heads=-2), "EINVAL"), (dict(kv_heads=0), "EINVAL"), (dict(q_heads=5), "EINVAL"),
+    (dict(head_dim=20), "EINVAL"), (dict(head_dim=136), "EINVAL"), (dict(pages=-1), "EINVAL"), (dict(page_size=0), "EINVAL"),
+    (dict(page_size=8), "EINVAL"), (dict(page_size=24), "EINVAL"), (dict(table_width=-1), "EINVAL"), (dict(table_width=1 << 26), "EINVAL"),
+    (dict(q_len=1 << 30), "EINVAL"), (dict(batch=1 << 24), "EINVAL"), (dict(scale=0.0), "EINVAL"), (dict(scale=float("inf")), "EINVAL"),
+    (dict(f16=2), "EINVAL"), (dict(q_stride=(256, 256, -64)), "EINVAL"), (dict(q_stride=(250, 256, 64)), "EINVAL"), (dict(k_stride=(2048, 1 << 23, 64)), "EINVAL"),
+    (dict(v_stride=(2048, 56, 64)), "EINVAL"), (dict(k_stride=(2050, 128, 64)), "EINVAL"), (dict(out_stride=(256, 256, 0)), "EINVAL"),
+    (dict(out_stride=(128, 256, 64)), "EINVAL"), (dict(table_stride=-4), "EINVAL"), (dict(q=0), "EINVAL"), (dict(k_cache=0), "EINVAL"),
+    (dict(table=0), "EINVAL"), (dict(lens=0), "EINVAL"), (dict(out=0), "EINVAL"), (dict(q=0x10000008), "EALIGN"), (dict(v_cache=0x30000002), "EALIGN"),
+    (dict(table=0x50000002), "EALIGN"), (dict(lens=0x51000001), "EALIGN"), (dict(lse=0x60000002), "EALIGN"), (dict(out=0x10000010), "EOVERLAP"),
+    (dict(out=0x20000010), "EOVERLAP"), (dict(table=0x40000010), "EOVERLAP"), (dict(lse=0x40000010), "EOVERLAP"), (dict(lse=0x51000000), "EOVERLAP"),
+    (CUT, "ESCRATCH"), (dict(CUT, workspace=0x60000000, workspace_bytes=8), "ESCRATCH"), (dict(CUT, workspace=0x60000008, workspace_bytes=1 << 28), "EALIGN"),
+    (dict(CUT, workspace=0x30000000, workspace_bytes=1 << 28), "EOVERLAP")])
+def test_paged_refuses(over, code):
+    assert w4.paged_attention_raw(paged(**over), 0) == getattr(w4, code)
+
+
+@pytest.mark.parametrize("over", [
+    dict(), dict(lse=0x60000000), dict(table_width=0, table=0, k_cache=0), dict(pages=0, v_cache=0), dict(k_cache=0x30000000), dict(table_stride=0),
+    dict(CUT, workspace=0x60000000, workspace_bytes=1 << 28), dict(pages=1, k_stride=(3, 128, 64)), dict(page_size=48)])
+def test_paged_accepts(over):
+    assert w4.paged_attention_raw(paged(**over), 0) in REACHED
+
+
+def test_paged_empty_null_and_workspace():
+    run, need = w4.paged_attention_raw, w4.paged_attention_workspace
+    assert run(paged(batch=0, q=0), 0) == w4.OK and run(paged(q_len=0), 0) == w4.OK and run(paged(q_heads=0), 0) == w4.OK
+    lib = w4._native.load()
+    assert lib.paged_attention(None, None) == w4.EINVAL and lib.paged_attention_workspace(None) == w4.EINVAL
+    assert need(paged()) == 0 and need(paged(**CUT)) > 0 and need(paged(page_size=8)) == w4.EINVAL and need(paged(table_width=0)) == 0
+
+
+@pytest.mark.parametrize("page", [16, 32, 48, 80, 112, 1008, 4112, 2**20 - 16, 2**29])
+def test_page_of_a_key(page):
+    """The multiplier by which the kernel divides, at every border, for keys below 2^31."""
+    n = 4
+    while 1 << n < page:
+        n += 1
+    magic = ((1 << (31 + n)) + page - 1) // page
+    assert magic < 2**32
+    keys = [k for m in list(range(0, 70)) + [2**31 // page // 3, 2**31 // page - 1, 2**31 // page] for k in (m * page - 1, m * page, m * page + page - 1)]
+    for k in keys + [2**31 - 1]:
+        if 0 <= k < 2**31:
+            assert (k * magic >> 32) >> (n - 1) == k // page
+
+
 # ---------------------------------------------------------------- the Python checks
 
 def test_python_checks():
@@ -151,7 +246,8 @@ def test_python_checks():
         w4.cache_append(*(z(1, 1, 8, dtype=bf) for _ in range(4)), z(1, dtype=torch.int64))
 
 
-STRUCTURES = {"block_norm_t": "BlockNormArgs", "lora_adapters_t": "LoraAdaptersArgs", "cache_append_t": "CacheAppendArgs"}
+STRUCTURES = {"block_norm_t": "BlockNormArgs", "lora_adapters_t": "LoraAdaptersArgs", "packed_attention_t": "PackedAttentionArgs",
+              "paged_attention_t": "PagedAttentionArgs", "cache_append_t": "CacheAppendArgs"}
 
 
 def test_structures_match_the_header(tmp_path):
