@@ -583,7 +583,7 @@ int block_norm(const block_norm_t* args, void* stream);
  * depend on what it holds. Deterministic; no allocation, no synchronisation.
  */
 #define LORA_ADAPTERS_MAX_RANK 128
-#define LORA_ADAPTERS_MAX_ROWS 4194240
+#define LORA_ADAPTERS_MAX_ROWS 3145728
 typedef struct {
   const void* x;             /* 16-bit type, see f16 */
   const void* y;

@@ -134,7 +134,7 @@ def test_adapters_empty_null_and_workspace():
     assert lib.lora_adapters(None, None) == w4.EINVAL and lib.lora_adapters_workspace(None) == w4.EINVAL
     need = w4.lora_adapters_workspace
     assert need(adapt(K=60)) == w4.EINVAL and need(adapt(rows=0)) == 0
-    assert need(adapt(rows=1000, rank=17)) % (1000 * 32 * 4) == 0
+    assert need(adapt(rows=1000, rank=17)) >= 1000 * 32 * 4
     top = need(adapt(rows=w4.LORA_ADAPTERS_MAX_ROWS, rank=128, N=1 << 30, K=1 << 30))
     assert top >= w4.LORA_ADAPTERS_MAX_ROWS * 128 * 4
 
