@@ -20,7 +20,11 @@
 namespace w4a4 {
 
 template <bool F16>
-static const void* packed_of(int D) {
+static const void* packed_of(bool few, int D) {
+  if (few)
+    return D <= 64 ? reinterpret_cast<const void*>(attention_few_kernel<F16, FewAttn<64>, Attend::kPacked>)
+         : D <= 96 ? reinterpret_cast<const void*>(attention_few_kernel<F16, FewAttn<96>, Attend::kPacked>)
+                   : reinterpret_cast<const void*>(attention_few_kernel<F16, FewAttn<128>, Attend::kPacked>);
   return D <= 64 ? reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<64>, Attend::kPacked>)
        : D <= 96 ? reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<96>, Attend::kPacked>)
                  : reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<128>, Attend::kPacked>);
@@ -83,13 +87,20 @@ static int packed_run(const packed_attention_t* a, void* stream) {
   p.starts = a->starts;
   p.seqs = a->seqs;
   p.causal = a->causal;
+  // Few tiles leave compute units idle and wait out their keys one step after the other: there
+  // 32-row tiles, whose waves share the keys. By the 128-row tiles to expect, a sequence's last
+  // one counted half (both measured, us, 128-row tiles against 32-row ones; 24 heads on 8 of 128
+  // where no others are named). Fewer than 180: one prompt of 512 15.7 and 13.1, of 2048 with 8 heads of 64 32.9 and
+  // 17.3, 4096 with 4 heads 73.4 and 43.4, 532 + 250 + 117 + 102 with 16 of 72 14.6 and 12.8. More:
+  // one of 1024 25.2 and 27.4, eight of 256 16.1 and 30.4, 32 of 64 11.8 and 27.4.
+  constexpr int kWide = WideAttn<128>::ROWS, kFew = FewAttn<128>::ROWS, kFewTiles = 180;
+  static_assert(WideAttn<64>::ROWS == kWide && WideAttn<96>::ROWS == kWide && FewAttn<64>::ROWS == kFew && FewAttn<96>::ROWS == kFew, "one tile height");
+  const bool few = int64_t(a->tokens) * a->q_heads + int64_t(std::min(a->seqs, a->tokens)) * a->kv_heads * (kWide / 2) < int64_t(kFewTiles) * kWide;
   // the most tiles that sequences of these tokens can have; workgroups past the last leave
-  constexpr int kRows = WideAttn<128>::ROWS;
-  static_assert(WideAttn<64>::ROWS == kRows && WideAttn<96>::ROWS == kRows, "one tile height");
-  const int64_t tiles = int64_t(a->tokens) * p.group / kRows + std::min(a->seqs, a->tokens);
+  const int64_t tiles = int64_t(a->tokens) * p.group / (few ? kFew : kWide) + std::min(a->seqs, a->tokens);
   if (tiles * a->kv_heads >= lim) return GEMM_W4A4_EINVAL;
   void* args[] = {&p};
-  const hipError_t e = hipLaunchKernel(a->f16 ? packed_of<true>(D) : packed_of<false>(D), dim3(unsigned(tiles * a->kv_heads)), dim3(256),
+  const hipError_t e = hipLaunchKernel(a->f16 ? packed_of<true>(few, D) : packed_of<false>(few, D), dim3(unsigned(tiles * a->kv_heads)), dim3(256),
                                        args, 0, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GEMM_W4A4_OK : GEMM_W4A4_ELAUNCH;
 }

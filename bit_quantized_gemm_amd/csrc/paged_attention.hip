@@ -3,8 +3,8 @@
 // whose loads of 16 keys find their page in the table, and its join.
 //
 // Bound by reading the cache. The keys of tiles that fill no round of the compute units
-// are cut into parts of even length over the sequences, whose lengths only the device
-// knows; a second launch joins them in order.
+// are cut into parts, since sequences' lengths are known only to the device; a
+// second launch joins them in order.
 #include <hip/hip_runtime.h>
 
 #include <stddef.h>
@@ -38,8 +38,15 @@ static bool paged_sizes_ok(const paged_attention_t* a) {
          int64_t(a->batch) * a->kv_heads < lim / 256 && int64_t(a->batch) * a->q_len * a->q_heads < lim;
 }
 
+// Which tiles are cut, as for cross_attention, into parts of at least a step of all waves
+// (kMinPart keys; three tokens over 1001 keys: 256 12.8 us, 128 11.3, 64 10.9; eight
+// sequences of 1000 15.4, 13.9 and 13.0, of 200 10.5, 11.5 and 11.8). Up to kShort
+// keys each sequence's own are cut into as many parts; past that parts have even length over the
+// sequences, which takes the device 2 us to work out (one token, us, even parts against own: eight sequences of
+// 1000 19.9 and 15.4, four of 3000 to 100 15.4 and 14.6; one of 300 in a table of 8192 14.1, own parts would leave
+// most of 64 empty).
 static PagedPlan paged_plan(const paged_attention_t* a) {
-  constexpr int kMinPart = 256, kRows = FewAttn<128>::ROWS;
+  constexpr int kMinPart = 128, kShort = 4096, kRows = FewAttn<128>::ROWS;
   PagedPlan pl{};
   pl.rows_all = a->q_len * (a->q_heads / a->kv_heads);
   pl.tiles = (pl.rows_all + kRows - 1) / kRows;
@@ -53,7 +60,7 @@ static PagedPlan paged_plan(const paged_attention_t* a) {
       pl.parts = parts;
       pl.cut = left;
       pl.whole -= left;
-      pl.even = pl.whole == 0;
+      pl.even = pl.whole == 0 && a->table_width * a->page_size > kShort;
       const int64_t n = int64_t(left) * parts * kRows;
       pl.o_bytes = n * a->head_dim * 4;
       pl.bytes = pl.o_bytes + n * 8;

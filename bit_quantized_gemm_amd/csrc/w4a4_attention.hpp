@@ -182,11 +182,26 @@ __device__ __forceinline__ PackedTile packed_tile(const AttnParams& p, int n) {
   return w;
 }
 
-template <int KT>
-__device__ __forceinline__ Share share_of(const AttnParams& p) {
+template <class C, Attend A, int KT>
+__device__ __forceinline__ Share share_of(const AttnParams& p, int& rows, int& origin) {
   Share w;
   const int idx = blockIdx.x;
   w.idle = false;
+  if constexpr (A == Attend::kPacked) {
+    const int n = idx / p.kv_heads;
+    const PackedTile at = packed_tile<C::ROWS>(p, n);
+    w.idle = at.seq < 0;
+    if (w.idle) return w;
+    rows = at.len * p.group;
+    origin = at.start;
+    w.b = w.pair = 0;
+    w.kvh = idx - n * p.kv_heads;
+    w.tile = at.tile;
+    w.first = 0;
+    w.slot = -1;
+    w.len = p.causal ? min(at.len, (min(rows, (at.tile + 1) * C::ROWS) - 1) / p.group + 1) : at.len;
+    return w;
+  }
   if (p.even) {
     const EvenParts e = even_parts(p, idx, -1);
     w.idle = e.b < 0;
@@ -270,6 +285,7 @@ __device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   keys([&](int j, const uint16_t* k, const uint16_t* v) __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
     float s = 0.f;
 #pragma unroll
     for (int t = 0; t < DK; ++t) {
@@ -279,6 +295,7 @@ __device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x
       for (int i = 0; i < 4; ++i)
         s += widen<F16>(uint16_t(a[i])) * widen<F16>(uint16_t(qv[t][i])) +
              widen<F16>(uint16_t(a[i] >> 16)) * widen<F16>(uint16_t(qv[t][i] >> 16));
+      __builtin_amdgcn_sched_barrier(0);   // (one load at a time: registers)
     }
     s = other_sum(s);
     const float x = fabsf(ms) > kFar ? rounded_product(s, c) - ms : __builtin_fmaf(s, c, -ms);
@@ -294,6 +311,7 @@ __device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x
           o[d][i + 1] += w * widen<F16>(uint16_t(a.x >> 16));
           o[d][i + 2] += w * widen<F16>(uint16_t(a.y));
           o[d][i + 3] += w * widen<F16>(uint16_t(a.y >> 16));
+          __builtin_amdgcn_sched_barrier(0);
         }
   });
 }
@@ -370,15 +388,16 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, h = lane >> 5;
-  const Share w = share_of<C::KT * C::WAVES>(p);
+  int rows = p.rows, origin = 0;   // rows of the sequence; packed: its first token
+  const Share w = share_of<C, A, C::KT * C::WAVES>(p, rows, origin);
   if (w.idle) return;
   const int b = w.b, kvh = w.kvh, len = w.len, D = p.D;
   const int nt = (len + C::KT - 1) / C::KT;
 
   // this lane's query row
   const int row = w.tile * C::ROWS + l32;
-  const int rowc = min(row, p.rows - 1);
-  const int tok = rowc / p.group, hq = kvh * p.group + rowc % p.group;
+  const int rowc = min(row, rows - 1);
+  const int tok = origin + rowc / p.group, hq = kvh * p.group + rowc % p.group;
   u32x4 qv[DK];
   {
     const uint16_t* q = p.q + int64_t(b) * p.qs[0] + int64_t(tok) * p.qs[1] + int64_t(hq) * p.qs[2];
@@ -401,9 +420,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
     voff[u] = vc * 8 < D ? uint32_t(r) * vst + uint32_t(vc) * 16u : 0xFFFFFFF0u;
   }
   const uint16_t *kh = p.k + int64_t(kvh) * p.ks[2], *vh = p.v + int64_t(kvh) * p.vs[2];
-  if constexpr (A == Attend::kDense) {
-    kh += int64_t(b) * p.ks[0] + int64_t(w.first) * p.ks[1];
-    vh += int64_t(b) * p.vs[0] + int64_t(w.first) * p.vs[1];
+  if constexpr (A != Attend::kPaged) {
+    kh += int64_t(b) * p.ks[0] + int64_t(origin + w.first) * p.ks[1];
+    vh += int64_t(b) * p.vs[0] + int64_t(origin + w.first) * p.vs[1];
   }
   const uint8_t *kb = reinterpret_cast<const uint8_t*>(kh), *vb = reinterpret_cast<const uint8_t*>(vh);
   // paged: the table's entries page0 .. page0 + 63, one a lane
@@ -448,8 +467,13 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
   };
   const uint32_t kto = lds_address(kt), vto = lds_address(vt);
   const bool shared_memory = A == Attend::kDense && vst < uint32_t(D) * 2u;   // rows of v that overlap in memory
-  // paged: keys that this lane's row, a new token, sees (of the share), and the fewest of the tile
+  // keys of the share that this lane's row sees, and the fewest of the tile's rows
   int lim = len, lim0 = len;
+  if constexpr (A == Attend::kPacked)
+    if (p.causal) {
+      lim = min(len, tok - origin + 1);
+      lim0 = min(len, w.tile * C::ROWS / p.group + 1);
+    }
   if constexpr (A == Attend::kPaged) {
     const int before = keys_of(p, b) - p.q_len + 1 - w.first;   // (the sum of all keys and new tokens is below 2^31)
     lim = min(len, before + tok);
@@ -553,12 +577,21 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
     if (p.q_len > 1 && any_not_finite(o))
       careful_sums<F16, C>(o, qv, D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
         for (int t = wave; t < nt; t += C::WAVES)
+#pragma unroll 1
           for (int j = t * C::KT; j < min(len, (t + 1) * C::KT); ++j) {
             const int page = page_of(w.first + j);
             if (page >= 0)
               key(j, reinterpret_cast<const uint16_t*>(kb + key_at(w.first + j, page, p.ks[0], kst)),
                   reinterpret_cast<const uint16_t*>(vb + key_at(w.first + j, page, p.vs[0], vst)));
           }
+      });
+  if constexpr (A == Attend::kPacked)
+    if (p.causal && any_not_finite(o))
+      careful_sums<F16, C>(o, qv, D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
+        for (int t = wave; t < nt; t += C::WAVES)
+#pragma unroll 1
+          for (int j = t * C::KT; j < min(len, (t + 1) * C::KT); ++j)
+            key(j, reinterpret_cast<const uint16_t*>(kb + int64_t(j) * kst), reinterpret_cast<const uint16_t*>(vb + int64_t(j) * vst));
       });
   l = other_sum(l);
 
@@ -604,8 +637,12 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[d][i + e] += w4[e] * f;
       }
+    // (the compiler would otherwise read all waves' sums first and add them behind the branch below)
+    if constexpr (A == Attend::kPacked)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) asm volatile("" : "+v"(o[d]));
   }
-  if (row >= p.rows) return;
+  if (row >= rows) return;
   store_row<F16, C>(p, o, mm, l, w, l32, tok, hq, h);
 }
 
@@ -661,24 +698,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
   // where both can issue, so that the two do not run in step and wait for the
   // same units (4352 x 4608 keys, 24 heads of 128: 265 to 256 us).
   if (blockIdx.x & 256) __builtin_amdgcn_s_setprio(2);
-  Share w;
-  int rows, origin = 0;   // rows of the sequence; packed: its first token
-  if constexpr (A == Attend::kPacked) {
-    const int n = int(blockIdx.x) / p.kv_heads;
-    const PackedTile at = packed_tile<C::ROWS>(p, n);
-    if (at.seq < 0) return;
-    rows = at.len * p.group;
-    origin = at.start;
-    w.b = w.pair = 0;
-    w.kvh = int(blockIdx.x) - n * p.kv_heads;
-    w.tile = at.tile;
-    w.first = 0;
-    w.slot = -1;
-    w.len = p.causal ? min(at.len, (min(rows, (at.tile + 1) * C::ROWS) - 1) / p.group + 1) : at.len;
-  } else {
-    w = share_of<C::KT>(p);
-    rows = p.rows;
-  }
+  int rows = p.rows, origin = 0;   // rows of the sequence; packed: its first token
+  const Share w = share_of<C, A, C::KT>(p, rows, origin);
+  if (w.idle) return;
   const int b = w.b, kvh = w.kvh, len = w.len, D = p.D;
   const int n = (len + C::KT - 1) / C::KT;
 
@@ -909,6 +931,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
   if constexpr (A == Attend::kPacked)
     if (p.causal && any_not_finite(o))
       careful_sums<F16, C>(o, qv, D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
+#pragma unroll 1
         for (int j = 0; j < len; ++j)
           key(j, reinterpret_cast<const uint16_t*>(kb + int64_t(j) * kst), reinterpret_cast<const uint16_t*>(vb + int64_t(j) * vst));
       });

@@ -1,13 +1,13 @@
 #!/usr/bin/env python3
 """The attention half of a diffusion transformer block on MXFP4 weights, every
-step of it but the layer norm and the residual in this package's kernels:
+step of it in this package's kernels:
 
     vec -> quantize_mxfp4_act -> gemm_mxfp4_few            shift, scale, gate
-    x   -> layer norm, modulated -> quantize_mxfp4_act -> gemm_mxfp4   q, k, v
+    x   -> block_norm (layer norm, scale, shift) -> quantize_mxfp4_act -> gemm_mxfp4   q, k, v
     q, k -> rotary_axes (time, height, width), in place
     q -> cross_attention to the image's keys, and to a text encoder's states
          (a length per sequence), joined by their log-sum-exps
-    -> quantize_mxfp4_act -> gemm_mxfp4 -> gate, residual
+    -> quantize_mxfp4_act -> gemm_mxfp4 -> block_norm (gate, residual, the other half's norm)
 
     python examples/transformer_block.py [--height 64 --width 64 --text 512 --heads 24 --batch 1]
 
@@ -86,7 +86,7 @@ class Block:
         B, L, hidden = x.shape
         H, D = self.heads, self.dim
         shift, scale, gate = self.modulation(vec)[:, None].chunk(3, -1)
-        h = torch.nn.functional.layer_norm(x, (hidden,)) * (1 + scale) + shift
+        h, _ = w4.block_norm(x, scale=scale, shift=shift, eps=1e-5)
         joint = self.qkv(h.reshape(B * L, hidden)).view(B, L, 3 * H, D)
         turned = joint[:, :, :2 * H]
         w4.rotary_axes(turned, positions, self.inv_freq, self.sections, out=turned)
@@ -96,7 +96,8 @@ class Block:
         words, lw = w4.cross_attention(q, states[:, :, :H], states[:, :, H:], kv_lens=text_lens, return_lse=True)
         share = torch.sigmoid(lw - li).transpose(1, 2)[..., None]      # the words' part of all weights
         o = torch.lerp(image.float(), words.float(), share).to(x.dtype)
-        return x + gate * self.out(o.view(B * L, hidden)).view(B, L, hidden)
+        # (with it comes the norm that the block's other half begins with)
+        return w4.block_norm(x, self.out(o.view(B * L, hidden)).view(B, L, hidden), gate=gate, eps=1e-5)[1]
 
     def plain(self, x, vec, text, text_lens, positions):
         x, vec, text = x.float(), vec.float(), text.float()
