@@ -389,9 +389,14 @@ __global__ __launch_bounds__(512) void adapters_join_kernel(const AdaptParams p)
 // to be transposed, D[column][row] = up^T low^T, and D through the same LDS back to rows,
 // so that y and out are read and written 128 bytes a row (straight from the
 // accumulators, 32 bytes a row at a time, 4352 x 12288 columns took 99 us).
-// KT: steps of 16 ranks at most. TAIL: N is no multiple of 8. SLICED: low as the slices' sums.
+// KT: steps of 16 ranks at most. SLICED: low as the slices' sums.
 // blockIdx: 4 waves of columns, row tile, slot.
-template <bool F16, int KT, bool TAIL, bool SLICED>
+enum class Tail {
+  kNone,     // N is a multiple of 8
+  kShift,
+  kNarrow,   // N is below 8
+};
+template <bool F16, int KT, Tail TAIL, bool SLICED>
 __global__ __launch_bounds__(256, KT > 4 ? (SLICED ? 1 : 2) : SLICED ? 2 : KT > 2 ? 3 : 4) void adapters_expand_kernel(const AdaptParams p) {
   constexpr int ROWB = 128, PITCH = 68;   // bytes of a row of up's tile; floats of a row of D
   constexpr int BYTES = KT * 16 * ROWB > 32 * PITCH * 4 ? KT * 16 * ROWB : 32 * PITCH * 4;
@@ -404,23 +409,32 @@ __global__ __launch_bounds__(256, KT > 4 ? (SLICED ? 1 : 2) : SLICED ? 2 : KT > 
   float* sums = reinterpret_cast<float*>(tile);
   const int row0 = SLICED ? blockIdx.y * 64 : 0;
   const int r8 = lane >> 3, c8 = lane & 7, n = n0 + 8 * c8;   // accesses of rows: 8 lanes a row
-  // columns n .. n + 7 of a row; those past N are not stored, and zeros or others of the row
+  // Columns n .. n + 7 of a row; those past N are not stored, and whatever the row holds. The loads of
+  // the last columns end with the row and are moved down afterwards (`settle`), so that every load is
+  // one access, and certain.
   auto load8 = [&](const uint16_t* row) __attribute__((always_inline)) {
-    if constexpr (TAIL) {
+    if constexpr (TAIL == Tail::kNarrow) {
       u32x4 v{0u, 0u, 0u, 0u};
-      if (n + 8 <= p.N) v = load16_any(row + n);
-      else
 #pragma unroll
-        for (int i = 0; i < 7; ++i)
-          if (n + i < p.N) v[i >> 1] |= uint32_t(row[n + i]) << (16 * (i & 1));
+      for (int i = 0; i < 7; ++i)
+        if (n + i < p.N) v[i >> 1] |= uint32_t(row[n + i]) << (16 * (i & 1));
       return v;
     } else {
       return load16_any(row + min(n, p.N - 8));
     }
   };
+  const bool last = TAIL == Tail::kShift && n0 + 64 > p.N;   // the wave holds the row's end
+  auto settle = [&](u32x4& v) __attribute__((always_inline)) {
+    if constexpr (TAIL == Tail::kShift) {
+      const int by = max(n + 8 - p.N, 0);
+      if (by & 1) v = u32x4{v.x >> 16 | v.y << 16, v.y >> 16 | v.z << 16, v.z >> 16 | v.w << 16, v.w >> 16};
+      if (by & 2) v = u32x4{v.y, v.z, v.w, 0u};
+      if (by & 4) v = u32x4{v.z, v.w, 0u, 0u};
+    }
+  };
   auto store8 = [&](uint16_t* row, u32x4 v) __attribute__((always_inline)) {
     if (n + 8 <= p.N) store16_any(row + n, v);
-    else if constexpr (TAIL)
+    else if constexpr (TAIL != Tail::kNone)
 #pragma unroll
       for (int i = 0; i < 7; ++i)
         if (n + i < p.N) row[n + i] = uint16_t(v[i >> 1] >> (16 * (i & 1)));
@@ -437,6 +451,7 @@ __global__ __launch_bounds__(256, KT > 4 ? (SLICED ? 1 : 2) : SLICED ? 2 : KT > 
 #pragma unroll
       for (int i = 0; i < 2 * NT; ++i) {
         const int r = 8 * i + r8;
+        if (last) settle(in[i]);
         if (r >= rank) in[i] = u32x4{0u, 0u, 0u, 0u};
         *reinterpret_cast<u32x4*>(tile + r * ROWB + (c8 ^ ((r >> 1 & 1) << 2)) * 16) = in[i];
       }
@@ -459,7 +474,11 @@ __global__ __launch_bounds__(256, KT > 4 ? (SLICED ? 1 : 2) : SLICED ? 2 : KT > 
         at[i] = row0 + of_lane(places, min(base + 8 * i + r8, count - 1));
         yv[i] = load8(p.y + at[i] * p.ys);
       }
-      if constexpr (NT > 0) {
+      if constexpr (NT == 0) {
+        if (last)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) settle(yv[i]);
+      } else {
         f32x16 acc[2] = {};
         float back = 1.f;
         const int row = row0 + of_lane(places, min(base + l32, count - 1));   // of this lane's column of D
@@ -521,6 +540,9 @@ __global__ __launch_bounds__(256, KT > 4 ? (SLICED ? 1 : 2) : SLICED ? 2 : KT > 
               acc[d] = mfma32<F16>(up[d][k], lv[k][1], acc[d]);
             }
         }
+        if (last)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) settle(yv[i]);
         // D to rows (a wave's LDS accesses keep their order)
 #pragma unroll
         for (int d = 0; d < 2; ++d)
@@ -637,7 +659,7 @@ static const void* shrink_of(bool many, int ranks) {
                      : reinterpret_cast<const void*>(adapters_shrink_kernel<F16, 8, 1, 8>);
 }
 
-template <bool F16, bool TAIL, bool SLICED>
+template <bool F16, Tail TAIL, bool SLICED>
 static const void* expand_of(int ranks) {
   return ranks <= 16 ? reinterpret_cast<const void*>(adapters_expand_kernel<F16, 1, TAIL, SLICED>)
        : ranks <= 32 ? reinterpret_cast<const void*>(adapters_expand_kernel<F16, 2, TAIL, SLICED>)
@@ -645,10 +667,15 @@ static const void* expand_of(int ranks) {
                      : reinterpret_cast<const void*>(adapters_expand_kernel<F16, 8, TAIL, SLICED>);
 }
 
+template <bool F16, bool SLICED>
+static const void* expand_of(int ranks, int N) {
+  if (N < 8) return reinterpret_cast<const void*>(adapters_expand_kernel<F16, 8, Tail::kNarrow, SLICED>);
+  return N % 8 == 0 ? expand_of<F16, Tail::kNone, SLICED>(ranks) : expand_of<F16, Tail::kShift, SLICED>(ranks);
+}
+
 template <bool F16>
-static const void* expand_of(int ranks, bool tail, bool sliced) {
-  return tail ? (sliced ? expand_of<F16, true, true>(ranks) : expand_of<F16, true, false>(ranks))
-              : (sliced ? expand_of<F16, false, true>(ranks) : expand_of<F16, false, false>(ranks));
+static const void* expand_of(int ranks, int N, bool sliced) {
+  return sliced ? expand_of<F16, true>(ranks, N) : expand_of<F16, false>(ranks, N);
 }
 
 static int lora_adapters_run(const lora_adapters_t* a, void* stream) {
@@ -716,9 +743,8 @@ static int lora_adapters_run(const lora_adapters_t* a, void* stream) {
   if (e == hipSuccess && pl.many)
     e = hipLaunchKernel(a->f16 ? reinterpret_cast<const void*>(adapters_join_kernel<true>) : reinterpret_cast<const void*>(adapters_join_kernel<false>),
                         dim3(unsigned((a->rows + 31) / 32)), dim3(pl.Rp * 4), args, 0, st);
-  const bool tail = a->N % 8 != 0;
   if (e == hipSuccess)
-    e = hipLaunchKernel(a->f16 ? expand_of<true>(a->rank, tail, !pl.many) : expand_of<false>(a->rank, tail, !pl.many),
+    e = hipLaunchKernel(a->f16 ? expand_of<true>(a->rank, a->N, !pl.many) : expand_of<false>(a->rank, a->N, !pl.many),
                         dim3(unsigned((a->N + 255) / 256), unsigned(pl.out_tiles), unsigned(pl.out_slots)), dim3(256), args, 0, st);
   return e == hipSuccess ? GEMM_W4A4_OK : GEMM_W4A4_ELAUNCH;
 }
