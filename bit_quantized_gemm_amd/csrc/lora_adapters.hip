@@ -609,16 +609,20 @@ static bool adapt_sizes_ok(const lora_adapters_t* a) {
          a->rank >= 1 && a->rank <= LORA_ADAPTERS_MAX_RANK && a->adapters >= 1;
 }
 
+// Few or many by rows x rank x columns, since few rows split low anew for every 64 columns. Both
+// measured (us, few against many), up to 2^26: 800 rows, rank 16, 1024 columns 10.3 and 16.0, 431,
+// 32, 2746 10.3 and 17.4, 1200, 16, 3072 16.1 and 18.7, 512, 32, 3072 18.7 and 17.9; past it 260, 64, 7822
+// 21.6 and 20.1, 300, 64, 9216 28.8 and 19.6, 512, 32, 12288 25.6 and 21.3, 150, 128, 12288 32 and 25.
 // Few rows: workgroups of 16 rows, one for each distinct adapter, and slices of K of at least
 // 512 (a turn for each wave) while there are fewer workgroups than compute units. Many: the
 // groups' tiles (of 64 ranks and 64 rows the operands are loaded once for 16 products; past rank
 // 64 two workgroups of 32 rows a tile), slices of about 512, all of whose loads are in flight at once,
 // up to two workgroups a compute unit.
 static AdaptPlan adapt_plan(const lora_adapters_t* a) {
-  constexpr int kFewValues = 384 * 32;
+  constexpr int64_t kFewWork = int64_t(1) << 26;
   AdaptPlan pl{};
   pl.Rp = 16 * rank_steps(a->rank);
-  pl.many = int64_t(a->rows) * pl.Rp > kFewValues && a->adapters <= kGroupAdapters;
+  pl.many = a->rows > 64 && int64_t(a->rows) * pl.Rp * a->N > kFewWork && a->adapters <= kGroupAdapters;
   if (pl.many) {
     pl.out_tiles = a->rows / 64 + std::min(a->adapters + 1, a->rows);
     pl.out_slots = 1;
