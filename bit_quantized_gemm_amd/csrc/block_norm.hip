@@ -6,12 +6,13 @@
 //   h = (norm(r) weight + bias) (1 + scale) + shift
 //
 // Bound by memory: x and y are read once, r and h written once, about 16 flops
-// an element. A row's values stay in its lanes' registers from the loads to the
+// an element. 4096 x 3072, layer norm with gate, scale and shift: 16.4 us, 6.2 TB/s of
+// reads and writes (a 1 GiB copy: 5.1); 4352 x 12288 82.9, 5.2 TB/s. A row's values stay in its lanes' registers from the loads to the
 // stores, in float32; both norms' statistics are taken from them there (the
 // variance from the differences to the mean, not from a difference of sums).
 //
-// A row is a wave's, or four waves' where the row is long or rows are few. Rows
-// of any width start on any 2-byte boundary; all accesses are 16 bytes, the last
+// A row is a wave's, or four waves' where the row is long or rows are few, or 16
+// lanes' where it is short and rows are many. Rows of any width start on any 2-byte boundary; all accesses are 16 bytes, the last
 // one of a width that is no multiple of 8 over the last 8 elements, the ones
 // that it shares with its neighbour left out of the sums (both lanes store
 // the same value for them).
@@ -44,15 +45,16 @@ struct RowStats {
   float pre, mean, rstd;
 };
 
-// WAVES waves a row, CH runs of 8 elements a lane. TAIL: the width is no multiple of 8.
-template <bool F16, bool LAYER, int WAVES, int CH, bool TAIL>
+// LANES lanes a row, CH runs of 8 elements a lane. TAIL: the width is no multiple of 8.
+template <bool F16, bool LAYER, int LANES, int CH, bool TAIL>
 __global__ __launch_bounds__(256) void block_norm_kernel(const NormParams p) {
-  constexpr int LANES = 64 * WAVES, ROWS = 256 / LANES;   // rows of a workgroup
+  constexpr int WAVES = LANES / 64, ROWS = 256 / LANES;   // waves of a row (0: less than one); rows of a workgroup
   __shared__ float part[2][4];
   const int tid = threadIdx.x, wave = tid >> 6;
   const int lane = tid & (LANES - 1);
-  const int row = __builtin_amdgcn_readfirstlane(int(blockIdx.x) * ROWS + (WAVES == 1 ? wave : 0));
-  if (WAVES == 1 && row >= p.rows) return;   // (a workgroup of four waves has one row)
+  int row = int(blockIdx.x) * ROWS + tid / LANES;
+  if constexpr (WAVES > 0) row = __builtin_amdgcn_readfirstlane(row);
+  if (ROWS > 1 && row >= p.rows) return;   // (nothing below meets other rows' lanes)
   const int b = row / p.tokens, tok = row - b * p.tokens;
   const int C = p.width, runs = (C + 7) >> 3;
 
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(256) void block_norm_kernel(const NormParams p) {
   };
   int turn = 0;
   auto row_sum = [&](float v) __attribute__((always_inline)) {
-    v = wave_sum(v);
+    v = WAVES == 0 ? sum_of_16(v) : wave_sum(v);
     if constexpr (WAVES > 1) {
       // (two places in turn: a wave may still read the last sum's while another writes the next)
       if ((tid & 63) == 0) part[turn][wave] = v;
@@ -242,19 +244,23 @@ __global__ __launch_bounds__(256) void block_norm_kernel(const NormParams p) {
 
 // ------------------------------------------------------------------ host side
 
+template <bool F16, bool LAYER, bool TAIL, int LANES>
+static const void* norm_kernel_of(int ch) {
+  if constexpr (LANES == 16)
+    return reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 16, 1, TAIL>);
+  else
+    return ch <= 1 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, LANES, 1, TAIL>)
+         : ch <= 2 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, LANES, 2, TAIL>)
+         : ch <= 4 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, LANES, 4, TAIL>)
+         : ch <= 6 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, LANES, 6, TAIL>)
+                   : reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, LANES, 8, TAIL>);
+}
+
 template <bool F16, bool LAYER, bool TAIL>
-static const void* norm_kernel_of(int waves, int ch) {
-  if (waves == 1)
-    return ch <= 1 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 1, 1, TAIL>)
-         : ch <= 2 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 1, 2, TAIL>)
-         : ch <= 4 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 1, 4, TAIL>)
-         : ch <= 6 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 1, 6, TAIL>)
-                   : reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 1, 8, TAIL>);
-  return ch <= 1 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 4, 1, TAIL>)
-       : ch <= 2 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 4, 2, TAIL>)
-       : ch <= 4 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 4, 4, TAIL>)
-       : ch <= 6 ? reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 4, 6, TAIL>)
-                 : reinterpret_cast<const void*>(block_norm_kernel<F16, LAYER, 4, 8, TAIL>);
+static const void* norm_kernel_of(int lanes, int ch) {
+  return lanes == 16 ? norm_kernel_of<F16, LAYER, TAIL, 16>(ch)
+       : lanes == 64 ? norm_kernel_of<F16, LAYER, TAIL, 64>(ch)
+                     : norm_kernel_of<F16, LAYER, TAIL, 256>(ch);
 }
 
 static int block_norm_run(const block_norm_t* a, void* stream) {
@@ -262,6 +268,7 @@ static int block_norm_run(const block_norm_t* a, void* stream) {
   if ((a->f16 | 1) != 1 || (a->layer | 1) != 1 || (a->post_norm | 1) != 1) return GEMM_W4A4_EINVAL;
   if (!(a->eps >= 1e-12f && a->eps <= 1.f) || !(fabsf(a->residual_scale) < INFINITY)) return GEMM_W4A4_EINVAL;
   if (int64_t(a->batch) * a->tokens >= (int64_t(1) << 31)) return GEMM_W4A4_EINVAL;
+  if (a->batch == 0 || a->tokens == 0) return GEMM_W4A4_OK;   // (tensors without elements may have no address)
   if (!a->y && (a->gate || a->residual || a->post_norm || a->residual_scale != 1.f)) return GEMM_W4A4_EINVAL;
   if (a->post_weight && !a->post_norm) return GEMM_W4A4_EINVAL;
   const int C = a->width, size[3] = {a->batch, a->tokens, 1};
@@ -283,7 +290,6 @@ static int block_norm_run(const block_norm_t* a, void* stream) {
     t.extent = t.p ? strided_extent(size, st, C) : 0;
     if (t.extent < 0 || (t.p && !strides_apart(size, st, C))) return GEMM_W4A4_EINVAL;
   }
-  if (a->batch == 0 || a->tokens == 0) return GEMM_W4A4_OK;
   if (!a->x || !a->out) return GEMM_W4A4_EINVAL;
   uintptr_t all = uintptr_t(a->weight) | uintptr_t(a->bias) | uintptr_t(a->post_weight);
   for (const Tensor& t : in) all |= uintptr_t(t.p);
@@ -331,18 +337,23 @@ static int block_norm_run(const block_norm_t* a, void* stream) {
   p.eps = a->eps;
   p.width_f = float(C);
   p.post = a->post_norm;
-  const int waves = C > 4096 || p.rows < 4 * kNumCUs ? 4 : 1;
-  const int ch = (C + 512 * waves - 1) / (512 * waves);
+  // Lanes of a row. All sides measured (us, with y, gate, scale and shift). 16 against 64: 98304 x 128 19.0 and
+  // 42.8, 24672 x 115 7.5 and 16.3, 1100 x 128 3.1 and 3.5. 256 against 64: 8 x 3072 3.6 and 5.3, 600 x
+  // 3072 5.4 and 6.3, 1100 x 4096 8.5 and 10.3, 2000 x 4096 12.8 and 14.5; 2000 x 2048 8.0 and 7.8, 4096 x 3072 20.1
+  // and 17.1, 4096 x 1001 11.9 and 8.5.
+  const bool few = p.rows < 4 * kNumCUs || (C > 2048 && p.rows <= 8 * kNumCUs);
+  const int lanes = C > 4096 || few ? 256 : C <= 128 ? 16 : 64;
+  const int ch = (C + 8 * lanes - 1) / (8 * lanes);
   const bool tail = C % 8 != 0;
   const void* k;
   if (a->f16)
-    k = a->layer ? (tail ? norm_kernel_of<true, true, true>(waves, ch) : norm_kernel_of<true, true, false>(waves, ch))
-                 : (tail ? norm_kernel_of<true, false, true>(waves, ch) : norm_kernel_of<true, false, false>(waves, ch));
+    k = a->layer ? (tail ? norm_kernel_of<true, true, true>(lanes, ch) : norm_kernel_of<true, true, false>(lanes, ch))
+                 : (tail ? norm_kernel_of<true, false, true>(lanes, ch) : norm_kernel_of<true, false, false>(lanes, ch));
   else
-    k = a->layer ? (tail ? norm_kernel_of<false, true, true>(waves, ch) : norm_kernel_of<false, true, false>(waves, ch))
-                 : (tail ? norm_kernel_of<false, false, true>(waves, ch) : norm_kernel_of<false, false, false>(waves, ch));
+    k = a->layer ? (tail ? norm_kernel_of<false, true, true>(lanes, ch) : norm_kernel_of<false, true, false>(lanes, ch))
+                 : (tail ? norm_kernel_of<false, false, true>(lanes, ch) : norm_kernel_of<false, false, false>(lanes, ch));
   void* args[] = {&p};
-  const int per = 4 / waves;
+  const int per = 256 / lanes;
   const hipError_t e = hipLaunchKernel(k, dim3(unsigned((int64_t(p.rows) + per - 1) / per)), dim3(256), args, 0,
                                        static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GEMM_W4A4_OK : GEMM_W4A4_ELAUNCH;

@@ -19,11 +19,15 @@ __device__ __forceinline__ float lane_permuted(float v) {
 
 // The sum over the wave, in every lane, always in the same order. In registers:
 // shuffles through LDS take five times as long (a chain of six of about 100 cycles).
-__device__ __forceinline__ float wave_sum(float v) {
+__device__ __forceinline__ float sum_of_16(float v) {   // over each 16 lanes
   v += lane_permuted<0xB1>(v);    // lane ^ 1
   v += lane_permuted<0x4E>(v);    // lane ^ 2
   v += lane_permuted<0x141>(v);   // the other 4 of 8
   v += lane_permuted<0x140>(v);   // the other 8 of 16
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = sum_of_16(v);
   auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
   v = __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
   r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
