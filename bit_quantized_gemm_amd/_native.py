@@ -261,7 +261,7 @@ ATTENTION_MAX_HEAD_DIM = 128
 BLOCK_NORM_MAX_WIDTH = 16384
 LORA_ADAPTERS_MAX_RANK = 128
 LORA_ADAPTERS_MAX_ROWS = 3145728
-PACKED_ATTENTION_MAX_SEQS = 1 << 20
+PACKED_ATTENTION_MAX_SEQS = 4096
 PAGED_ATTENTION_PAGE_MULTIPLE = 16
 
 

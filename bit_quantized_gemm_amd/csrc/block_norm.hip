@@ -22,6 +22,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "gemm_w4a4.h"
 #include "w4a4_common.hpp"
 #include "w4a4_half.hpp"
@@ -52,9 +54,10 @@ __global__ __launch_bounds__(256) void block_norm_kernel(const NormParams p) {
   __shared__ float part[2][4];
   const int tid = threadIdx.x, wave = tid >> 6;
   const int lane = tid & (LANES - 1);
-  int row = int(blockIdx.x) * ROWS + tid / LANES;
+  const int64_t nth = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * ROWS + tid / LANES;
+  if (nth >= p.rows) return;   // (nothing below meets other rows' lanes)
+  int row = int(nth);
   if constexpr (WAVES > 0) row = __builtin_amdgcn_readfirstlane(row);
-  if (ROWS > 1 && row >= p.rows) return;   // (nothing below meets other rows' lanes)
   const int b = row / p.tokens, tok = row - b * p.tokens;
   const int C = p.width, runs = (C + 7) >> 3;
 
@@ -353,8 +356,9 @@ static int block_norm_run(const block_norm_t* a, void* stream) {
     k = a->layer ? (tail ? norm_kernel_of<false, true, true>(lanes, ch) : norm_kernel_of<false, true, false>(lanes, ch))
                  : (tail ? norm_kernel_of<false, false, true>(lanes, ch) : norm_kernel_of<false, false, false>(lanes, ch));
   void* args[] = {&p};
-  const int per = 256 / lanes;
-  const hipError_t e = hipLaunchKernel(k, dim3(unsigned((int64_t(p.rows) + per - 1) / per)), dim3(256), args, 0,
+  // (a dimension of a launch holds fewer than 2^32 threads)
+  const int64_t groups = (int64_t(p.rows) * lanes + 255) / 256, wide = std::min(groups, int64_t(1) << 20);
+  const hipError_t e = hipLaunchKernel(k, dim3(unsigned(wide), unsigned((groups + wide - 1) / wide)), dim3(256), args, 0,
                                        static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GEMM_W4A4_OK : GEMM_W4A4_ELAUNCH;
 }

@@ -63,6 +63,19 @@ static int packed_run(const packed_attention_t* a, void* stream) {
     for (const auto& i : ins)
       if (overlaps(o.p, o.n, i.p, i.n)) return GEMM_W4A4_EOVERLAP;
   if (overlaps(outs[0].p, outs[0].n, outs[1].p, outs[1].n)) return GEMM_W4A4_EOVERLAP;
+  const int group = a->q_heads / a->kv_heads;
+  // Few tiles leave compute units idle and wait out their keys one step after the other: there
+  // 32-row tiles, whose waves share the keys. By the 128-row tiles to expect, a sequence's last
+  // one counted half (both measured, us, 128-row tiles against 32-row ones; 24 heads on 8 of 128
+  // where no others are named). Fewer than 180: one prompt of 512 15.7 and 13.1, of 2048 with 8 heads of 64 32.9 and
+  // 17.3, 4096 with 4 heads 73.4 and 43.4, 532 + 250 + 117 + 102 with 16 of 72 14.6 and 12.8. More:
+  // one of 1024 25.2 and 27.4, eight of 256 16.1 and 30.4, 32 of 64 11.8 and 27.4.
+  constexpr int kWide = WideAttn<128>::ROWS, kFew = FewAttn<128>::ROWS, kFewTiles = 180;
+  static_assert(WideAttn<64>::ROWS == kWide && WideAttn<96>::ROWS == kWide && FewAttn<64>::ROWS == kFew && FewAttn<96>::ROWS == kFew, "one tile height");
+  const bool few = int64_t(a->tokens) * a->q_heads + int64_t(std::min(a->seqs, a->tokens)) * a->kv_heads * (kWide / 2) < int64_t(kFewTiles) * kWide;
+  // the most tiles that sequences of these tokens can have; workgroups past the last leave
+  const int64_t tiles = int64_t(a->tokens) * group / (few ? kFew : kWide) + std::min(a->seqs, a->tokens);
+  if (tiles * a->kv_heads >= int64_t(1) << 24) return GEMM_W4A4_EINVAL;   // (a launch holds fewer than 2^32 threads)
   const int dev_rc = check_device();
   if (dev_rc != GEMM_W4A4_OK) return dev_rc;
 
@@ -82,23 +95,11 @@ static int packed_run(const packed_attention_t* a, void* stream) {
   p.q_len = p.kv_len = a->tokens;
   p.kv_heads = a->kv_heads;
   p.D = D;
-  p.group = a->q_heads / a->kv_heads;
+  p.group = group;
   p.c = a->scale * 1.4426950408889634f;
   p.starts = a->starts;
   p.seqs = a->seqs;
   p.causal = a->causal;
-  // Few tiles leave compute units idle and wait out their keys one step after the other: there
-  // 32-row tiles, whose waves share the keys. By the 128-row tiles to expect, a sequence's last
-  // one counted half (both measured, us, 128-row tiles against 32-row ones; 24 heads on 8 of 128
-  // where no others are named). Fewer than 180: one prompt of 512 15.7 and 13.1, of 2048 with 8 heads of 64 32.9 and
-  // 17.3, 4096 with 4 heads 73.4 and 43.4, 532 + 250 + 117 + 102 with 16 of 72 14.6 and 12.8. More:
-  // one of 1024 25.2 and 27.4, eight of 256 16.1 and 30.4, 32 of 64 11.8 and 27.4.
-  constexpr int kWide = WideAttn<128>::ROWS, kFew = FewAttn<128>::ROWS, kFewTiles = 180;
-  static_assert(WideAttn<64>::ROWS == kWide && WideAttn<96>::ROWS == kWide && FewAttn<64>::ROWS == kFew && FewAttn<96>::ROWS == kFew, "one tile height");
-  const bool few = int64_t(a->tokens) * a->q_heads + int64_t(std::min(a->seqs, a->tokens)) * a->kv_heads * (kWide / 2) < int64_t(kFewTiles) * kWide;
-  // the most tiles that sequences of these tokens can have; workgroups past the last leave
-  const int64_t tiles = int64_t(a->tokens) * p.group / (few ? kFew : kWide) + std::min(a->seqs, a->tokens);
-  if (tiles * a->kv_heads >= lim) return GEMM_W4A4_EINVAL;
   void* args[] = {&p};
   const hipError_t e = hipLaunchKernel(a->f16 ? packed_of<true>(few, D) : packed_of<false>(few, D), dim3(unsigned(tiles * a->kv_heads)), dim3(256),
                                        args, 0, static_cast<hipStream_t>(stream));

@@ -96,6 +96,7 @@ static int paged_run(const paged_attention_t* a, void* stream) {
   if ((uintptr_t(a->q) | uintptr_t(a->out) | (keys ? uintptr_t(a->k_cache) | uintptr_t(a->v_cache) : 0u)) & 15u) return GEMM_W4A4_EALIGN;
   if ((uintptr_t(a->lse) | uintptr_t(a->lens) | (keys ? uintptr_t(a->table) : 0u)) & 3u) return GEMM_W4A4_EALIGN;
   const PagedPlan pl = paged_plan(a);
+  if (pl.whole >= int64_t(1) << 24) return GEMM_W4A4_EINVAL;   // (a launch holds fewer than 2^32 threads)
   if (pl.bytes > 0) {
     if (!a->workspace || a->workspace_bytes < pl.bytes) return GEMM_W4A4_ESCRATCH;
     if (uintptr_t(a->workspace) & 15u) return GEMM_W4A4_EALIGN;
@@ -158,7 +159,6 @@ static int paged_run(const paged_attention_t* a, void* stream) {
   void* args[] = {&p, &tile_rows};
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t grid = pl.whole + int64_t(pl.cut) * pl.parts;
-  if (grid >= (int64_t(1) << 31)) return GEMM_W4A4_EINVAL;
   hipError_t e = hipLaunchKernel(a->f16 ? paged_of<true>(D) : paged_of<false>(D), dim3(unsigned(grid)), dim3(256), args, 0, st);
   if (e == hipSuccess && pl.cut > 0) {
     const int rows = std::min(tile_rows, pl.rows_all);

@@ -140,45 +140,87 @@ __device__ __forceinline__ int packed_len(const AttnParams& p, int s) { return m
 // Packed sequences: workgroups take key heads, and for each the row tiles of all sequences
 // by their place in the sequence, the last ones first: with the mask these have the most
 // keys, so that the longest work begins first. With F(t) tiles at place t or later, tile
-// number n of all is at the last place t with F(t) > n.
+// number n of all is at the last place t with F(t) > n, and there the one of the
+// (n - F(t + 1))-th sequence that has a tile at that place.
+//
+// Up to 64 sequences a lane of each wave has one; past that a thread of the workgroup has
+// kSeqs, and the waves' sums meet in LDS.
+constexpr int kSeqs = 16;
+static_assert(kSeqs * 256 == PACKED_ATTENTION_MAX_SEQS, "a place for every sequence");
 struct PackedTile {
   int seq, tile, start, len;   // seq < 0: past the last
 };
-template <int ROWS>
+template <int ROWS, bool MANY>
 __device__ __forceinline__ PackedTile packed_tile(const AttnParams& p, int n) {
-  const int lane = threadIdx.x & 63;
-  auto tiles_of = [&](int s) __attribute__((always_inline)) {
-    return s < p.seqs ? int((int64_t(packed_len(p, s)) * p.group + ROWS - 1) / ROWS) : 0;
+  constexpr int SEQS = MANY ? kSeqs : 1, WAVES = 4;
+  __shared__ int meet[2][WAVES];
+  __shared__ int found;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int own[SEQS];   // tiles of this thread's sequences
+#pragma unroll
+  for (int i = 0; i < SEQS; ++i) {
+    const int s = MANY ? tid + 256 * i : lane;
+    own[i] = s < p.seqs ? int((int64_t(packed_len(p, s)) * p.group + ROWS - 1) / ROWS) : 0;
+  }
+  int turn = 0;
+  auto sum = [&](int v) __attribute__((always_inline)) {
+    v = wave_sum_int(v);
+    if constexpr (MANY) {
+      // (two places in turn: a wave may still read the last sum's while another writes the next)
+      if (lane == 0) meet[turn][wave] = v;
+      __syncthreads();
+      v = __builtin_amdgcn_readfirstlane(meet[turn][0] + meet[turn][1] + meet[turn][2] + meet[turn][3]);
+      turn ^= 1;
+    }
+    return v;
   };
-  const int own = tiles_of(lane);   // of the first 64 sequences
   auto from = [&](int t) __attribute__((always_inline)) {
-    int f = max(own - t, 0);
-    for (int s = lane + 64; s < p.seqs; s += 64) f += max(tiles_of(s) - t, 0);
-    return wave_sum_int(f);
+    int f = 0;
+#pragma unroll
+    for (int i = 0; i < SEQS; ++i) f += max(own[i] - t, 0);
+    return sum(f);
   };
   PackedTile w{-1, 0, 0, 0};
-  int lo = 0, hi = int((int64_t(p.q_len) * p.group + ROWS - 1) / ROWS);   // F(hi) = 0
   if (n >= from(0)) return w;
+  int lo = 0, hi = int((int64_t(p.q_len) * p.group + ROWS - 1) / ROWS);   // F(hi) = 0
   while (hi - lo > 1) {
     const int mid = lo + (hi - lo) / 2;
     if (from(mid) > n) lo = mid;
     else hi = mid;
   }
-  int nth = n - from(lo + 1);   // among the sequences with a tile at this place
-  for (int c = 0; c < p.seqs; c += 64) {
-    const uint64_t has = __builtin_amdgcn_ballot_w64((c == 0 ? own : tiles_of(c + lane)) > lo);
-    const int count = __builtin_popcountll(has);
-    if (nth < count) {
-      const int rank = __builtin_popcountll(has & ((uint64_t(1) << lane) - 1));
-      const uint64_t hit = __builtin_amdgcn_ballot_w64((has >> lane & 1) && rank == nth);
-      w.seq = c + __builtin_ctzll(hit);
-      w.tile = lo;
-      w.start = __builtin_amdgcn_readfirstlane(packed_start(p, w.seq));
-      w.len = __builtin_amdgcn_readfirstlane(packed_len(p, w.seq));
-      return w;
+  const int nth = n - from(lo + 1);   // among the sequences with a tile at this place
+  if constexpr (!MANY) {
+    const uint64_t has = __builtin_amdgcn_ballot_w64(own[0] > lo);
+    const int rank = __builtin_popcountll(has & ((uint64_t(1) << lane) - 1));
+    const uint64_t hit = __builtin_amdgcn_ballot_w64((has >> lane & 1) && rank == nth);
+    if (hit == 0) return w;
+    w.seq = __builtin_ctzll(hit);
+  } else {
+    // by thread, and for a thread by its own order
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < SEQS; ++i) mine += own[i] > lo;
+    int upto = mine;   // of the wave's lanes up to this one
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(upto, d);
+      if (lane >= d) upto += v;
     }
-    nth -= count;
+    if (lane == 63) meet[turn][wave] = upto;
+    if (tid == 0) found = -1;
+    __syncthreads();
+    int before = upto - mine;
+    for (int v = 0; v < wave; ++v) before += meet[turn][v];
+#pragma unroll
+    for (int i = 0; i < SEQS; ++i)
+      if (own[i] > lo && before++ == nth) found = tid + 256 * i;
+    __syncthreads();
+    w.seq = __builtin_amdgcn_readfirstlane(found);
+    if (w.seq < 0) return w;
   }
+  w.tile = lo;
+  w.start = __builtin_amdgcn_readfirstlane(packed_start(p, w.seq));
+  w.len = __builtin_amdgcn_readfirstlane(packed_len(p, w.seq));
   return w;
 }
 
@@ -189,7 +231,7 @@ __device__ __forceinline__ Share share_of(const AttnParams& p, int& rows, int& o
   w.idle = false;
   if constexpr (A == Attend::kPacked) {
     const int n = idx / p.kv_heads;
-    const PackedTile at = packed_tile<C::ROWS>(p, n);
+    const PackedTile at = p.seqs <= 64 ? packed_tile<C::ROWS, false>(p, n) : packed_tile<C::ROWS, true>(p, n);
     w.idle = at.seq < 0;
     if (w.idle) return w;
     rows = at.len * p.group;
@@ -271,8 +313,8 @@ __device__ __forceinline__ float rounded_product(float a, float b) {
 
 // The sums o of a lane's row again, key by key, leaving out the keys that the row does
 // not see. In the matrix product those have weight 0, which is not enough where a value
-// is an infinity or a NaN: 0 times it is NaN. Taken when a sum is one; slow (some 300
-// instructions a key), and nothing but those values brings a program here.
+// is an infinity or a NaN: 0 times it is NaN. Taken when a sum is one and a value that some row
+// does not see is one; slow (some 300 instructions a key).
 // `key` calls its argument with every key's index and the addresses of its k and v rows.
 template <bool F16, class C, class F>
 __device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x4 (&qv)[C::DP / 16], int D, float c, float m,
@@ -314,6 +356,21 @@ __device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x
           __builtin_amdgcn_sched_barrier(0);
         }
   });
+}
+
+// Whether v holds an infinity or a NaN for the keys first .. last - 1 (`at`: a key's row).
+template <bool F16, class F>
+__device__ __forceinline__ bool keys_not_finite(int first, int last, int D, F&& at) {
+  const int e = 2 * (threadIdx.x & 63);
+  float z = 0.f;
+  for (int j = first; j < last; ++j) {
+    const uint16_t* v = at(j);
+    if (v && e < D) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(v + e);
+      z += widen<F16>(uint16_t(w)) * 0.f + widen<F16>(uint16_t(w >> 16)) * 0.f;
+    }
+  }
+  return __builtin_amdgcn_ballot_w64(!(z == 0.f)) != 0;
 }
 
 // Whether a sum of the wave's rows is an infinity or a NaN.
@@ -574,7 +631,11 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
   }
   wait_vm<0>();
   if constexpr (A == Attend::kPaged)
-    if (p.q_len > 1 && any_not_finite(o))
+    if (lim0 < len && any_not_finite(o) &&
+        keys_not_finite<F16>(max(lim0, 0), len, D, [&](int j) __attribute__((always_inline)) {
+          const int page = page_of(w.first + j);
+          return page < 0 ? nullptr : reinterpret_cast<const uint16_t*>(vb + key_at(w.first + j, page, p.vs[0], vst));
+        }))
       careful_sums<F16, C>(o, qv, D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
         for (int t = wave; t < nt; t += C::WAVES)
 #pragma unroll 1
@@ -586,7 +647,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
           }
       });
   if constexpr (A == Attend::kPacked)
-    if (p.causal && any_not_finite(o))
+    if (lim0 < len && any_not_finite(o) && keys_not_finite<F16>(lim0, len, D, [&](int j) __attribute__((always_inline)) {
+          return reinterpret_cast<const uint16_t*>(vb + int64_t(j) * vst);
+        }))
       careful_sums<F16, C>(o, qv, D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
         for (int t = wave; t < nt; t += C::WAVES)
 #pragma unroll 1
@@ -929,7 +992,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
   }
 
   if constexpr (A == Attend::kPacked)
-    if (p.causal && any_not_finite(o))
+    if (lim0 < len && any_not_finite(o) && keys_not_finite<F16>(lim0, len, D, [&](int j) __attribute__((always_inline)) {
+          return reinterpret_cast<const uint16_t*>(vb + int64_t(j) * vst);
+        }))
       careful_sums<F16, C>(o, qv, D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
 #pragma unroll 1
         for (int j = 0; j < len; ++j)

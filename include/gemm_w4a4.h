@@ -653,10 +653,10 @@ int cache_append(const cache_append_t* args, void* stream);
  *
  * scale, head_dim, heads, strides (token, head) and alignment as for cross_attention, v's
  * token stride at least head_dim; tokens * q_heads at most 2^31 - CROSS_ATTENTION_PAST_END; seqs up to
- * PACKED_ATTENTION_MAX_SEQS; kv_heads below 2^20. tokens, seqs or q_heads 0: nothing is
+ * PACKED_ATTENTION_MAX_SEQS; kv_heads below 2^20; tokens * q_heads / 128 + seqs * kv_heads below 2^24. tokens, seqs or q_heads 0: nothing is
  * enqueued. One launch, no workspace; deterministic.
  */
-#define PACKED_ATTENTION_MAX_SEQS (1 << 20)
+#define PACKED_ATTENTION_MAX_SEQS 4096
 typedef struct {
   const void* q;
   const void* k;
@@ -693,7 +693,7 @@ int packed_attention(const packed_attention_t* args, void* stream);
  * Arithmetic as for cross_attention.
  *
  * page_size a multiple of PAGED_ATTENTION_PAGE_MULTIPLE; table_width * page_size and q_len below
- * 2^30 - CROSS_ATTENTION_PAST_END; scale, head_dim, heads, strides (q and out: batch, token, head; caches: page,
+ * 2^30 - CROSS_ATTENTION_PAST_END; batch * kv_heads times the tiles of 32 rows of each below 2^24; scale, head_dim, heads, strides (q and out: batch, token, head; caches: page,
  * token, head; table: batch), alignment and limits of rows as for cross_attention, v_cache's token
  * stride at least head_dim. Made for few new tokens: every 32 rows (token, query head of
  * a key head) read the keys anew. batch, q_len or q_heads 0: nothing is enqueued; pages or

@@ -64,8 +64,8 @@ def test_shared_heads(HQ, HKV):
 def test_many_sequences():
     """More sequences than a wave has lanes, most of them short, some empty."""
     rng = np.random.default_rng(5)
-    for count in (64, 65, 129, 400):
-        lens = [int(n) for n in np.where(rng.random(count) < 0.2, 0, rng.integers(1, 12, count))]
+    for count in (64, 65, 129, 400, 4096):
+        lens = [int(n) for n in np.where(rng.random(count) < 0.2, 0, rng.integers(1, 12 if count < 4096 else 3, count))]
         lens[count // 2], lens[-1] = 300, 140
         check(*inputs(sum(lens) + 5, 4, 2, 64, "bf16"), starts_of(lens), f"{count} sequences")
 

@@ -149,7 +149,7 @@ def packed(**over):
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(tokens=-1), "EINVAL"), (dict(seqs=-1), "EINVAL"), (dict(seqs=(1 << 20) + 1), "EINVAL"), (dict(q_heads=-4), "EINVAL"),
+    (dict(tokens=-1), "EINVAL"), (dict(seqs=-1), "EINVAL"), (dict(seqs=4097), "EINVAL"), (dict(tokens=1 << 22, q_heads=500, kv_heads=500, q_stride=(32000, 64), k_stride=(32000, 64), v_stride=(32000, 64), out_stride=(32000, 64), k=1 << 44, v=1 << 45, out=1 << 46, starts=1 << 47, seqs=4096), "EINVAL"), (dict(q_heads=-4), "EINVAL"),
     (dict(kv_heads=0), "EINVAL"), (dict(q_heads=5), "EINVAL"), (dict(head_dim=0), "EINVAL"), (dict(head_dim=60), "EINVAL"),
     (dict(head_dim=136), "EINVAL"), (dict(scale=0.0), "EINVAL"), (dict(scale=float("nan")), "EINVAL"), (dict(causal=2), "EINVAL"),
     (dict(f16=-1), "EINVAL"), (dict(tokens=1 << 29), "EINVAL"), (dict(q_heads=1 << 20, kv_heads=1 << 20), "EINVAL"),
@@ -165,7 +165,7 @@ def test_packed_refuses(over, code):
 
 @pytest.mark.parametrize("over", [
     dict(), dict(causal=0, lse=0x60000000), dict(k=0x30000000), dict(k_stride=(0, 0), v_stride=(64, 0)), dict(tokens=1, v_stride=(8, 64)),
-    dict(seqs=1 << 20)])
+    dict(seqs=4096)])
 def test_packed_accepts(over):
     assert packed(**over) in REACHED
 
@@ -193,6 +193,7 @@ CUT = dict(table_width=400)
     (dict(head_dim=20), "EINVAL"), (dict(head_dim=136), "EINVAL"), (dict(pages=-1), "EINVAL"), (dict(page_size=0), "EINVAL"),
     (dict(page_size=8), "EINVAL"), (dict(page_size=24), "EINVAL"), (dict(table_width=-1), "EINVAL"), (dict(table_width=1 << 26), "EINVAL"),
     (dict(q_len=1 << 30), "EINVAL"), (dict(batch=1 << 24), "EINVAL"), (dict(scale=0.0), "EINVAL"), (dict(scale=float("inf")), "EINVAL"),
+    (dict(q_len=1 << 28, q_heads=2, kv_heads=1, out=1 << 45, lens=1 << 46, table=1 << 47), "EINVAL"),
     (dict(f16=2), "EINVAL"), (dict(q_stride=(256, 256, -64)), "EINVAL"), (dict(q_stride=(250, 256, 64)), "EINVAL"), (dict(k_stride=(2048, 1 << 23, 64)), "EINVAL"),
     (dict(v_stride=(2048, 56, 64)), "EINVAL"), (dict(k_stride=(2050, 128, 64)), "EINVAL"), (dict(out_stride=(256, 256, 0)), "EINVAL"),
     (dict(out_stride=(128, 256, 64)), "EINVAL"), (dict(table_stride=-4), "EINVAL"), (dict(q=0), "EINVAL"), (dict(k_cache=0), "EINVAL"),
