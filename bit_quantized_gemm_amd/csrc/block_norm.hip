@@ -64,21 +64,23 @@ __global__ __launch_bounds__(256) void block_norm_kernel(const NormParams p) {
   // Run c of a lane, the runs dealt from the row's end: only a lane's first run can be the
   // one that is cut, so that only it needs masks (with the runs dealt from the row's
   // start every run did, and 150 to 370 of them were spilled).
-  int at[CH], skip = 0;   // first element of a run; the cut run's elements that belong to the one before
-  bool live[CH];
+  int at[CH], skip = 0;   // first element of a run, negative past the row's start; the cut run's elements that belong to the one before
+  bool some[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int n = runs - 1 - (c * LANES + lane);
-    live[c] = n >= 0;
+    some[c] = n >= 0;
     at[c] = n * 8;
   }
   if (TAIL && at[0] + 8 > C) {
     skip = at[0] - max(0, C - 8);
     at[0] = max(0, C - 8);
   }
+  // (kept where no masks press: 4096 rows of 3072 16.4 us, 19.8 made anew each time)
+  auto live = [&](int c) __attribute__((always_inline)) { return TAIL ? at[c] >= 0 : some[c]; };
   // (fewer than 8 elements: one by one, the rest zeros that `in` leaves out)
   auto load = [&](const uint16_t* from, int c) __attribute__((always_inline)) {
-    if (!live[c]) return u32x4{0u, 0u, 0u, 0u};
+    if (!live(c)) return u32x4{0u, 0u, 0u, 0u};
     if (TAIL && c == 0 && C < 8) {
       u32x4 v{};
 #pragma unroll
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(256) void block_norm_kernel(const NormParams p) {
     return load16_any(from + at[c]);
   };
   auto store = [&](uint16_t* to, int c, u32x4 v) __attribute__((always_inline)) {
-    if (!live[c]) return;
+    if (!live(c)) return;
     if (TAIL && c == 0 && C < 8) {
 #pragma unroll
       for (int i = 0; i < 7; ++i)
@@ -101,7 +103,7 @@ __global__ __launch_bounds__(256) void block_norm_kernel(const NormParams p) {
   auto value = [](const u32x4& v, int i) __attribute__((always_inline)) { return widen<F16>(uint16_t(v[i >> 1] >> (16 * (i & 1)))); };
   // whether element i of run c counts in the sums
   auto in = [&](int c, int i) __attribute__((always_inline)) {
-    return live[c] && (!TAIL || c > 0 || (i >= skip && at[0] + i < C));
+    return live(c) && (!TAIL || c > 0 || (i >= skip && at[0] + i < C));
   };
   int turn = 0;
   auto row_sum = [&](float v) __attribute__((always_inline)) {
@@ -116,6 +118,12 @@ __global__ __launch_bounds__(256) void block_norm_kernel(const NormParams p) {
     return v;
   };
   auto stats_with = [&](const float (&v)[CH][8], float pre, float eps) __attribute__((always_inline)) {
+    // (the masks of the runs made anew: held from one step to the next, eight runs' were spilled)
+    if constexpr (TAIL) {
+      asm volatile("" : "+v"(skip));
+#pragma unroll
+      for (int c = 0; c < CH; ++c) asm volatile("" : "+v"(at[c]));
+    }
     RowStats s{pre, 0.f, 0.f};
     if constexpr (LAYER) {
       float sum = 0.f;

@@ -57,6 +57,14 @@ struct AttnParams {
   int page_shift;
 };
 
+// The parameters, read once more: what only the end of a kernel needs and would be kept over
+// its main loop (where the scalar registers are spilled) if it were taken from `p`.
+__device__ __forceinline__ const AttnParams& params_again() {
+  auto at = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  return *(const AttnParams*)at;
+}
+
 // What a workgroup does: keys first .. first + len - 1 for row tile `tile` of
 // (sequence, key head) `pair`. KT: keys are divided in multiples of it.
 struct Share {
@@ -293,6 +301,29 @@ struct FewAttn {
   static_assert(MERGE <= LDS && 2 * LDS <= kLdsLimit, "two workgroups a compute unit");
 };
 
+// Paged: the table's entries page0 .. page0 + 63 of sequence b, one a lane.
+struct Pages {
+  const AttnParams& p;
+  int b, page0 = 0, entries = -1;
+  __device__ __forceinline__ void look(int from) {
+    page0 = from;
+    const int64_t at = int64_t(from) + (threadIdx.x & 63);
+    entries = at * p.page_size < p.kv_len ? p.table[int64_t(b) * p.table_stride + at] : -1;
+  }
+  // the page that holds key `key` of the sequence: its number in the cache, -1 where there is none
+  __device__ __forceinline__ int page_of(int key) {
+    const int i = int(__umulhi(uint32_t(key), p.page_magic) >> p.page_shift);
+    if (i < page0 || i >= page0 + 64) look(i);
+    const int e = __builtin_amdgcn_readlane(entries, i - page0);
+    return e >= 0 && e < p.pages ? e : -1;
+  }
+  // the bytes from a cache's start to that key, `stride` a token
+  __device__ __forceinline__ int64_t key_at(int key, int page, int64_t page_stride, uint32_t stride) const {
+    const int i = int(__umulhi(uint32_t(key), p.page_magic) >> p.page_shift);
+    return int64_t(page) * page_stride * 2 + int64_t(key - i * p.page_size) * stride;
+  }
+};
+
 // Position of chunk c of row r.
 template <class C>
 __device__ __forceinline__ int k_chunk(int r, int c) { return c ^ (C::CH == 16 ? r & 15 : (r >> 1) & 7); }
@@ -327,12 +358,14 @@ __device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   keys([&](int j, const uint16_t* k, const uint16_t* v) __attribute__((always_inline)) {
+    int Dk = D;
+    asm volatile("" : "+s"(Dk));   // (the masks of the head size made here: kept over the keys they were spilled)
     __builtin_amdgcn_sched_barrier(0);
     float s = 0.f;
 #pragma unroll
     for (int t = 0; t < DK; ++t) {
       const int e = 16 * t + 8 * h;
-      const u32x4 a = e < D ? *reinterpret_cast<const u32x4*>(k + e) : u32x4{0u, 0u, 0u, 0u};
+      const u32x4 a = e < Dk ? *reinterpret_cast<const u32x4*>(k + e) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         s += widen<F16>(uint16_t(a[i])) * widen<F16>(uint16_t(qv[t][i])) +
@@ -348,7 +381,7 @@ __device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const int e = 32 * d + 2 * i + 4 * h;
-          const u32x2 a = e < D ? *reinterpret_cast<const u32x2*>(v + e) : u32x2{0u, 0u};
+          const u32x2 a = e < Dk ? *reinterpret_cast<const u32x2*>(v + e) : u32x2{0u, 0u};
           o[d][i] += w * widen<F16>(uint16_t(a.x));
           o[d][i + 1] += w * widen<F16>(uint16_t(a.x >> 16));
           o[d][i + 2] += w * widen<F16>(uint16_t(a.y));
@@ -382,6 +415,36 @@ __device__ __forceinline__ bool any_not_finite(const f32x16 (&o)[DT]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) z += o[d][i] * 0.f;
   return __builtin_amdgcn_ballot_w64(!(z == 0.f)) != 0;
+}
+
+// The sums of a wave that are no numbers again, if a value that some row does not see is
+// none. The wave's keys: every WAVES-th tile of the share from `wave` on.
+template <bool F16, class C, Attend A, int WAVES>
+__device__ __forceinline__ void see_again(f32x16 (&o)[C::DP / 32], const u32x4 (&qv)[C::DP / 16], const AttnParams& p, const Share& w,
+                                          int origin, float m, int lim, int lim0, int wave) {
+  int len = __builtin_amdgcn_readfirstlane(w.len);
+  asm volatile("" : "+s"(len));
+  Pages pages{p, w.b};
+  const uint16_t *k = p.k + int64_t(w.kvh) * p.ks[2], *v = p.v + int64_t(w.kvh) * p.vs[2];
+  if constexpr (A == Attend::kPaged) pages.look(w.first / p.page_size);
+  // key j of the share, nullptr on a page that is none
+  auto row = [&](const uint16_t* x, const int64_t (&stride)[3], int j) __attribute__((always_inline)) -> const uint16_t* {
+    if constexpr (A == Attend::kPaged) {
+      const int page = pages.page_of(w.first + j);
+      return page < 0 ? nullptr : x + pages.key_at(w.first + j, page, stride[0], uint32_t(stride[1]) * 2u) / 2;
+    } else {
+      return x + int64_t(origin + w.first + j) * stride[1];
+    }
+  };
+  if (!keys_not_finite<F16>(max(lim0, 0), len, p.D, [&](int j) __attribute__((always_inline)) { return row(v, p.vs, j); })) return;
+  careful_sums<F16, C>(o, qv, p.D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
+    for (int t = wave; t * C::KT < len; t += WAVES)
+#pragma unroll 1
+      for (int j = t * C::KT; j < min(len, (t + 1) * C::KT); ++j) {
+        const uint16_t* at = row(k, p.ks, j);
+        if (at) key(j, at, row(v, p.vs, j));
+      }
+  });
 }
 
 // A row's result from its sums o (values 8 (i / 4) + 4 h + i % 4 of each 32),
@@ -482,26 +545,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
     vh += int64_t(b) * p.vs[0] + int64_t(origin + w.first) * p.vs[1];
   }
   const uint8_t *kb = reinterpret_cast<const uint8_t*>(kh), *vb = reinterpret_cast<const uint8_t*>(vh);
-  // paged: the table's entries page0 .. page0 + 63, one a lane
-  int page0 = 0, entries = -1;
-  auto look = [&](int from) __attribute__((always_inline)) {
-    page0 = from;
-    const int64_t at = int64_t(from) + lane;
-    entries = at * p.page_size < p.kv_len ? p.table[int64_t(b) * p.table_stride + at] : -1;
-  };
-  // the page that holds key `key` of the sequence: its number in the cache, -1 where there is none
-  auto page_of = [&](int key) __attribute__((always_inline)) {
-    const int i = int(__umulhi(uint32_t(key), p.page_magic) >> p.page_shift);
-    if (i < page0 || i >= page0 + 64) look(i);
-    const int e = __builtin_amdgcn_readlane(entries, i - page0);
-    return e >= 0 && e < p.pages ? e : -1;
-  };
-  // the bytes from a cache's start to that key, `stride` a token
-  auto key_at = [&](int key, int page, int64_t page_stride, uint32_t stride) __attribute__((always_inline)) {
-    const int i = int(__umulhi(uint32_t(key), p.page_magic) >> p.page_shift);
-    return int64_t(page) * page_stride * 2 + int64_t(key - i * p.page_size) * stride;
-  };
-  if constexpr (A == Attend::kPaged) look(w.first / p.page_size);
+  Pages pages{p, b};
+  if constexpr (A == Attend::kPaged) pages.look(w.first / p.page_size);
   const uint8_t* kt = smem + wave * 2 * C::TILE;
   const uint8_t* vt = kt + C::TILE;
   // the 16 rows from `half` on of tile t (an empty range past the last key: the
@@ -513,8 +558,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
       uint32_t any = uint32_t(-rows >> 31);   // all ones where rows > 0
       int64_t at = int64_t(r0) * stride;
       if constexpr (A == Attend::kPaged) {
-        const int page = rows > 0 ? page_of(w.first + r0) : 0;
-        at = key_at(w.first + r0, page, page_stride, stride);
+        const int page = rows > 0 ? pages.page_of(w.first + r0) : 0;
+        at = pages.key_at(w.first + r0, page, page_stride, stride);
         if (page < 0) any = 0;
       }
       const u32x4 rs = range_desc(base + at, (uint32_t(rows - 1) * stride + uint32_t(D) * 2u) & any);
@@ -570,7 +615,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int key = w.first + t * C::KT + 16 * half;
-        if (key - w.first < len && page_of(key) < 0)
+        if (key - w.first < len && pages.page_of(key) < 0)
 #pragma unroll
           for (int i = 8 * half; i < 8 * half + 8; ++i) sc[i] = -INFINITY;
       }
@@ -630,32 +675,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
     load(vb, p.vs[0], vst, voff, t + C::WAVES, vto);
   }
   wait_vm<0>();
-  if constexpr (A == Attend::kPaged)
-    if (lim0 < len && any_not_finite(o) &&
-        keys_not_finite<F16>(max(lim0, 0), len, D, [&](int j) __attribute__((always_inline)) {
-          const int page = page_of(w.first + j);
-          return page < 0 ? nullptr : reinterpret_cast<const uint16_t*>(vb + key_at(w.first + j, page, p.vs[0], vst));
-        }))
-      careful_sums<F16, C>(o, qv, D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
-        for (int t = wave; t < nt; t += C::WAVES)
-#pragma unroll 1
-          for (int j = t * C::KT; j < min(len, (t + 1) * C::KT); ++j) {
-            const int page = page_of(w.first + j);
-            if (page >= 0)
-              key(j, reinterpret_cast<const uint16_t*>(kb + key_at(w.first + j, page, p.ks[0], kst)),
-                  reinterpret_cast<const uint16_t*>(vb + key_at(w.first + j, page, p.vs[0], vst)));
-          }
-      });
-  if constexpr (A == Attend::kPacked)
-    if (lim0 < len && any_not_finite(o) && keys_not_finite<F16>(lim0, len, D, [&](int j) __attribute__((always_inline)) {
-          return reinterpret_cast<const uint16_t*>(vb + int64_t(j) * vst);
-        }))
-      careful_sums<F16, C>(o, qv, D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
-        for (int t = wave; t < nt; t += C::WAVES)
-#pragma unroll 1
-          for (int j = t * C::KT; j < min(len, (t + 1) * C::KT); ++j)
-            key(j, reinterpret_cast<const uint16_t*>(kb + int64_t(j) * kst), reinterpret_cast<const uint16_t*>(vb + int64_t(j) * vst));
-      });
+  const AttnParams& pe = A == Attend::kDense ? p : params_again();
+  if constexpr (A != Attend::kDense)
+    if (lim0 < len && any_not_finite(o)) see_again<F16, C, A, C::WAVES>(o, qv, pe, w, origin, m, lim, lim0, wave);
   l = other_sum(l);
 
   // join the waves' keys: the others write their sums, maximum and sum; wave 0
@@ -706,7 +728,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
       for (int d = 0; d < DT; ++d) asm volatile("" : "+v"(o[d]));
   }
   if (row >= rows) return;
-  store_row<F16, C>(p, o, mm, l, w, l32, tok, hq, h);
+  store_row<F16, C>(pe, o, mm, l, w, l32, tok, hq, h);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -991,18 +1013,12 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
       o[i % DT] = mfma32<F16>(i < 2 ? va[i] : read_v(last, i), i / DT == 0 ? w0 : w1, o[i % DT]);
   }
 
+  const AttnParams& pe = A == Attend::kDense ? p : params_again();
   if constexpr (A == Attend::kPacked)
-    if (lim0 < len && any_not_finite(o) && keys_not_finite<F16>(lim0, len, D, [&](int j) __attribute__((always_inline)) {
-          return reinterpret_cast<const uint16_t*>(vb + int64_t(j) * vst);
-        }))
-      careful_sums<F16, C>(o, qv, D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
-#pragma unroll 1
-        for (int j = 0; j < len; ++j)
-          key(j, reinterpret_cast<const uint16_t*>(kb + int64_t(j) * kst), reinterpret_cast<const uint16_t*>(vb + int64_t(j) * vst));
-      });
+    if (lim0 < len && any_not_finite(o)) see_again<F16, C, A, 1>(o, qv, pe, w, origin, m, lim, lim0, 0);
   if (row >= rows) return;
   l = other_sum(l);
-  store_row<F16, C>(p, o, m, l, w, wave * 32 + l32, tok, hq, h);
+  store_row<F16, C>(pe, o, m, l, w, wave * 32 + l32, tok, hq, h);
 }
 
 // Joins the parts of the cut tiles' rows, in order: one thread per 4 values,
