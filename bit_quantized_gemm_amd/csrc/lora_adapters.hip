@@ -15,7 +15,7 @@
 // distinct adapters of its rows, each of which has a workgroup of its own while there are
 // compute units, and expand adds the slices and splits the sums (below) itself. Many rows are
 // first grouped, a launch of one workgroup: tiles of 64 rows of one adapter. (Tiles as
-// they come take 60 us in place of 43 for 4352 rows of 12 requests and 12288 columns: the last
+// they come take 60 us in place of 47 for 4352 rows of 12 requests and 12288 columns: the last
 // tiles, of short requests, go through six adapters one after the other.) There the slices are
 // added and split between the two products, once for all columns.
 //
@@ -224,9 +224,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void adapters_shrink_kernel(const Ad
   constexpr int PER = 64 / (16 * XT);   // workgroups of a group's tile
   const int row0 = XT > 1 ? 0 : blockIdx.x * 16, slice = blockIdx.y;
   const int units = (p.K + UNIT - 1) / UNIT;
-  // A wave's turns lie one after the other, so that the waves of all workgroups, which move in
-  // step, are spread over the row. (A few hundred bytes apart, with rows 6 KiB apart, they all meet
-  // in an eighth of the memory channels: 4352 rows, K 3072, 35 us.)
+  // a wave's turns lie one after the other in the row
   const int nth = slice * WAVES + wave, all = p.slices * WAVES;
   const int u0 = int(int64_t(units) * nth / all), u1 = int(int64_t(units) * (nth + 1) / all);
   // NT: the adapter's rank tiles, and NX: tiles of its rows, so that every load is certain (with
