@@ -155,3 +155,15 @@ def test_in_a_graph():
         eager = w4.block_norm(post_norm=True, **{k: v * (1 + i) for k, v in t.items()})
         torch.cuda.synchronize()
         assert torch.equal(kept[0], eager[0]) and torch.equal(kept[1], eager[1]) and torch.equal(held["x"], eager[1])
+
+
+def test_more_rows_than_a_launch_dimension():
+    """17 million short rows: what each gives does not depend on where it lies."""
+    rows, width = 17_000_005, 8
+    some = torch.randn(1009, width, device=DEV).bfloat16()
+    x = some[torch.arange(rows, device=DEV) % 1009]
+    want = w4.block_norm(some, kind="rms")[0]
+    got = w4.block_norm(x, kind="rms")[0]
+    for at in range(0, rows, 2_000_000):
+        n = min(2_000_000, rows - at)
+        assert torch.equal(got[at:at + n], want[torch.arange(at, at + n, device=DEV) % 1009])

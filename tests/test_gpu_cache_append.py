@@ -22,7 +22,8 @@ def case(T, H, D, page, pages, dtype="bf16", seed=0):
 
 @pytest.mark.parametrize("T,H,D,page,pages,dtype", [
     (1, 1, 8, 1, 1, "bf16"), (1, 8, 128, 16, 3, "f16"), (7, 3, 72, 5, 9, "bf16"), (64, 8, 128, 64, 4, "bf16"), (1001, 2, 64, 48, 40, "f16"),
-    (4352, 8, 128, 16, 300, "bf16"), (3, 100, 40, 7, 2, "f16"), (2500, 1, 8, 32, 100, "bf16")])
+    (4352, 8, 128, 16, 300, "bf16"), (3, 100, 40, 7, 2, "f16"), (2500, 1, 8, 32, 100, "bf16"),
+    (140000, 1, 8, 16, 9000, "f16")])
 def test_every_byte(T, H, D, page, pages, dtype):
     print(f"case: {T} {H}x{D} page {page} of {pages} {dtype}", flush=True)
     k, v, kc, vc, slots = case(T, H, D, page, pages, dtype)

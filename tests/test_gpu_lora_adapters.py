@@ -188,3 +188,35 @@ def test_many_rows_and_adapters():
     last = torch.tensor([2, 0, 2, 1], dtype=torch.int32, device=DEV)
     out = w4.lora_adapters(torch.zeros(4, 16, device=DEV, dtype=torch.bfloat16), one, big, torch.ones(3, 128, 16, device=DEV, dtype=torch.bfloat16), last)
     assert out[:, 0].tolist() == [64.0, 0.0, 64.0, 0.0] and bits_of(out).shape == (4, 16)
+
+
+@pytest.mark.parametrize("M,A,K,N,R,dtype", [
+    (20000, 7, 64, 256, 16, "bf16"),        # more rows than the grouping holds in registers
+    (700, 5000, 72, 8200, 9, "f16"),        # more adapters than it takes
+    (3000, 4096, 40, 1500, 3, "bf16"),      # as many as it takes, most with a row or none
+    (1500, 3, 520, 1001, 128, "f16"), (9000, 2, 8, 503, 33, "bf16")])
+def test_many_rows(M, A, K, N, R, dtype):
+    """Picked rows against the oracle, the same bytes each time, in place, and replayed from a graph."""
+    y, x, down, up, scaling = inputs(M, A, K, N, R, dtype)
+    ids = order("any", M, A)
+    first = w4.lora_adapters(y, x, down, up, ids, scaling=scaling)
+    pick = np.random.default_rng(M).permutation(M)[:150].tolist() + [0, M - 1]
+    use = ids[pick].tolist()
+    t = [values_of(v) for v in (y[pick], x[pick], torch.stack([down[max(a, 0)] for a in use]), torch.stack([up[max(a, 0)] for a in use]))]
+    s = np.array([float(scaling[max(a, 0)]) for a in use], dtype=np.float32)
+    want, bound = ref.lora_adapters_ref(*t, [i if a >= 0 else -1 for i, a in enumerate(use)], s, dtype=dtype)
+    assert_within(values_of(first[pick]), want, bound, f"{M} rows of {A}")
+    assert torch.equal(first[ids < 0], y[ids < 0])
+    for _ in range(3):
+        assert torch.equal(w4.lora_adapters(y, x, down, up, ids, scaling=scaling), first)
+    held, hid = y.clone(), ids.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept = w4.lora_adapters(held, x, down, up, hid, scaling=scaling, out=held)
+    for i in range(3):
+        held.copy_(y)
+        hid.copy_(ids.roll(i))
+        g.replay()
+        eager = w4.lora_adapters(y, x, down, up, ids.roll(i), scaling=scaling)
+        torch.cuda.synchronize()
+        assert torch.equal(kept, eager)

@@ -23,6 +23,11 @@ def starts_of(lens, first=0):
     return torch.tensor([first + sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device=DEV)
 
 
+def padded(T, HQ, wide):
+    """Tokens of a batch of T, or with so much padding behind them that 128-row tiles are taken."""
+    return max(T, 23040 // HQ + 1) if wide else T
+
+
 def check(q, k, v, starts, what, causal=True, scale=None):
     dtype = "f16" if q.dtype == torch.float16 else "bf16"
     out = torch.full_like(q, 3.0)
@@ -38,27 +43,30 @@ def check(q, k, v, starts, what, causal=True, scale=None):
 LENGTHS = [[1], [2, 1, 1], [31, 32, 33], [5, 0, 64, 0, 0, 127], [128, 129, 1], [257], [300, 7, 90, 1, 1, 200], [511, 513], [0, 0], [1000]]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("lens", LENGTHS, ids=lambda l: "-".join(map(str, l)))
-def test_lengths(lens, causal):
+def test_lengths(lens, causal, wide):
     T = sum(lens)
     for HQ, HKV, D, dtype in ((4, 2, 64, "bf16"), (3, 3, 128, "f16"), (8, 1, 40, "bf16")):
         print(f"case: {lens} {HQ}/{HKV} D{D} {dtype} causal {causal}", flush=True)
-        q, k, v = inputs(T + 9, HQ, HKV, D, dtype)
+        q, k, v = inputs(padded(T + 9, HQ, wide), HQ, HKV, D, dtype)
         check(q, k, v, starts_of(lens, 4), f"{lens}", causal)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("D", range(8, 129, 8))
-def test_head_sizes(D):
+def test_head_sizes(D, wide):
     for dtype in ("bf16", "f16"):
-        check(*inputs(230, 6, 2, D, dtype), starts_of([150, 80]), f"D{D} {dtype}")
+        check(*inputs(padded(230, 6, wide), 6, 2, D, dtype), starts_of([150, 80]), f"D{D} {dtype}")
 
 
 @pytest.mark.parametrize("HQ,HKV", [(1, 1), (7, 7), (5, 1), (24, 8), (16, 1), (33, 1), (64, 2), (130, 1)])
 def test_shared_heads(HQ, HKV):
     """Groups that do and do not divide a tile's rows, and one with more heads than a tile."""
     for causal in (True, False):
-        check(*inputs(333, HQ, HKV, 72, "bf16"), starts_of([200, 3, 130]), f"{HQ}/{HKV}", causal)
+        for wide in (True, False):
+            check(*inputs(padded(333, HQ, wide), HQ, HKV, 72, "bf16"), starts_of([200, 3, 130]), f"{HQ}/{HKV}", causal)
 
 
 def test_many_sequences():
@@ -124,24 +132,25 @@ def test_strides():
     assert torch.equal(one[:145], w4.packed_attention(q, k[:, :1], v[:, :1], starts)[:145])
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("D,HQ,HKV", [(64, 4, 2), (128, 3, 3), (72, 8, 1)])
-def test_what_a_row_does_not_see(D, HQ, HKV, dtype):
+def test_what_a_row_does_not_see(D, HQ, HKV, dtype, wide):
     """Infinities and NaN in later tokens, and in other sequences, change no earlier row; rows that see them say so."""
     lens = [70, 150, 260, 20]
     starts, T = starts_of(lens), sum(lens)
-    q, k, v = inputs(T, HQ, HKV, D, dtype)
+    q, k, v = inputs(padded(T, HQ, wide), HQ, HKV, D, dtype)
     y, _, bound, _, _ = ref.packed_attention_ref(*(values_of(t) for t in (q, k, v)), starts.cpu().numpy(), dtype=dtype)
     for tensor, token, value in ((v, 69, float("nan")), (v, 100, float("inf")), (k, 130, float("nan")), (v, 300, float("-inf")), (k, 400, float("inf")),
                                  (v, 480, float("nan")), (q, 222, float("nan"))):
         t = tensor.clone()
         t[token, :, D // 2] = value
-        got = w4.packed_attention(*(t if s is tensor else s for s in (q, k, v)), starts)
+        got = w4.packed_attention(*(t if s is tensor else s for s in (q, k, v)), starts)[:T]
         end = next(e for e in (70, 220, 480, 500) if token < e)
         others = torch.ones(T, dtype=torch.bool, device=DEV)
         others[token:(token + 1 if tensor is q else end)] = False
         rows = others.cpu().numpy()      # (those of the same tile take the slow way)
-        assert_within(values_of(got)[rows], y[rows], bound[rows], f"{token} {value}")
+        assert_within(values_of(got)[rows], y[:T][rows], bound[:T][rows], f"{token} {value}")
         if tensor is v:
             assert not torch.isfinite(got[token:end, :, D // 2]).any()
             assert torch.isfinite(got[token:end, :, :D // 2]).all()
@@ -152,8 +161,23 @@ def test_what_a_row_does_not_see(D, HQ, HKV, dtype):
 @pytest.mark.parametrize("dtype,size", [("bf16", 1e4), ("bf16", 1e8), ("f16", 150.0), ("f16", 3e3)])
 def test_large_scores(dtype, size):
     lens = [40, 200]
-    q, k, v = inputs(240, 2, 2, 64, dtype, std=1.0)
-    check((q.float() * size).to(q.dtype), k, v, starts_of(lens), f"{dtype} {size}", scale=1.0)
+    for wide in (False, True):
+        q, k, v = inputs(padded(240, 2, wide), 2, 2, 64, dtype, std=1.0)
+        check((q.float() * size).to(q.dtype), k, v, starts_of(lens), f"{dtype} {size}", scale=1.0)
+
+
+def test_past_32_bits():
+    """Tokens so far apart that a sequence passes 2^32 bytes several times."""
+    T, D, far = 1100, 64, 2**22
+    space = torch.empty(2, T * far, dtype=torch.bfloat16, device=DEV)               # 9 GB each; the result in its own
+    q, k, v = inputs(T, 4, 2, D, "bf16")
+    starts = starts_of([5, 1000, 95])
+    want = w4.packed_attention(q, k, v, starts)
+    spread = [space[i // 3].as_strided((T, t.shape[1], D), (far, D, 1), i // 3 * T * far + 4096 * i) for i, t in enumerate((q, k, v, q))]
+    for to, t in zip(spread, (q, k, v)):
+        to.copy_(t)
+    got = w4.packed_attention(*spread[:3], starts, out=spread[3])
+    assert torch.equal(got, want)
 
 
 def test_repeats_streams_and_graph():
