@@ -29,11 +29,13 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // the barrier that publishes the data. Written as an instruction because the
 // compiler, where it knows of such a load, waits for all of them before every
 // transposing LDS read, which leaves none in flight. M0, the LDS base, is set
-// here, one idle cycle before the load takes it. The compiler reserves M0 and takes
+// here, one idle cycle before the load takes it. Scalar registers that a vector instruction wrote
+// (the descriptor's, from a readfirstlane) are taken five cycles later at the earliest, which is what
+// the idle cycles before that are for: inside the text the compiler sees no load to keep apart. The compiler reserves M0 and takes
 // no note of it as clobbered, so a kernel that uses this may have no other
 // instruction that sets or takes M0 (tests/test_block_asm.py reads the assembly).
 __device__ __forceinline__ void load_to_lds(const u32x4& desc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(desc)
+  asm volatile("s_nop 2\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(desc)
                : "memory");
 }
 
