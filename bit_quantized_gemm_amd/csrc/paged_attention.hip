@@ -1,8 +1,9 @@
 // paged_attention.hip — attention of each sequence's newest tokens over a paged
-// cache (paged_attention in gemm_w4a4.h): the few-row kernel of w4a4_attention.hpp,
-// whose loads of 16 keys find their page in the table, and its join.
+// cache (paged_attention in gemm_w4a4.h): the kernels of w4a4_attention.hpp,
+// whose loads of 16 keys find their page in the table, and their join.
 //
-// Bound by reading the cache. The keys of tiles that fill no round of the compute units
+// Few new tokens are bound by reading the cache, pieces of prompts by the matrix cores (2048 tokens
+// of 24 heads over 8000 keys: 221 us, 780 TFLOP/s of the unmasked scores). The keys of tiles that fill no round of the compute units
 // are cut into parts, since sequences' lengths are known only to the device; a
 // second launch joins them in order.
 #include <hip/hip_runtime.h>
@@ -20,6 +21,8 @@
 namespace w4a4 {
 
 struct PagedPlan {
+  bool few;     // 32-row tiles, waves over the keys
+  int rows;     // rows of a tile
   int tiles, rows_all;
   int64_t whole;
   int cut, parts;
@@ -46,10 +49,18 @@ static bool paged_sizes_ok(const paged_attention_t* a) {
 // 1000 19.9 and 15.4, four of 3000 to 100 15.4 and 14.6; one of 300 in a table of 8192 14.1, own parts would leave
 // most of 64 empty).
 static PagedPlan paged_plan(const paged_attention_t* a) {
-  constexpr int kMinPart = 128, kShort = 4096, kRows = FewAttn<128>::ROWS;
+  constexpr int kShort = 4096;
+  // 32-row tiles read the keys again for every 32 rows, but split them over their waves (us, 32-row
+  // tiles against 128-row ones, 24 heads on 8 where no others are named): 64 rows of 2 sequences of 4000, 8 heads
+  // of 64 14.4 and 15.8, 48 rows of 32 of 1000 31.4 and 30.6; 66 rows of 8 of 1000 22.4 and 19.8, 120 of
+  // 32 59 and 32, 1536 over 4096 keys 74 and 50, over 512 19.7 and 22.2, 6144 over 8000 472 and 221.
+  constexpr int kFewRows = 64;
   PagedPlan pl{};
   pl.rows_all = a->q_len * (a->q_heads / a->kv_heads);
-  pl.tiles = (pl.rows_all + kRows - 1) / kRows;
+  pl.few = pl.rows_all <= kFewRows;
+  pl.rows = pl.few ? FewAttn<128>::ROWS : WideAttn<128>::ROWS;
+  const int kMinPart = pl.few ? 128 : 256;
+  pl.tiles = (pl.rows_all + pl.rows - 1) / pl.rows;
   pl.whole = int64_t(pl.tiles) * a->batch * a->kv_heads;
   pl.parts = 1;
   const int left = int(pl.whole % kNumCUs);
@@ -61,7 +72,7 @@ static PagedPlan paged_plan(const paged_attention_t* a) {
       pl.cut = left;
       pl.whole -= left;
       pl.even = pl.whole == 0 && a->table_width * a->page_size > kShort;
-      const int64_t n = int64_t(left) * parts * kRows;
+      const int64_t n = int64_t(left) * parts * pl.rows;
       pl.o_bytes = n * a->head_dim * 4;
       pl.bytes = pl.o_bytes + n * 8;
     }
@@ -70,7 +81,11 @@ static PagedPlan paged_plan(const paged_attention_t* a) {
 }
 
 template <bool F16>
-static const void* paged_of(int D) {
+static const void* paged_of(bool few, int D) {
+  if (!few)
+    return D <= 64 ? reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<64>, Attend::kPaged>)
+         : D <= 96 ? reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<96>, Attend::kPaged>)
+                   : reinterpret_cast<const void*>(attention_wide_kernel<F16, WideAttn<128>, Attend::kPaged>);
   return D <= 64 ? reinterpret_cast<const void*>(attention_few_kernel<F16, FewAttn<64>, Attend::kPaged>)
        : D <= 96 ? reinterpret_cast<const void*>(attention_few_kernel<F16, FewAttn<96>, Attend::kPaged>)
                  : reinterpret_cast<const void*>(attention_few_kernel<F16, FewAttn<128>, Attend::kPaged>);
@@ -96,7 +111,9 @@ static int paged_run(const paged_attention_t* a, void* stream) {
   if ((uintptr_t(a->q) | uintptr_t(a->out) | (keys ? uintptr_t(a->k_cache) | uintptr_t(a->v_cache) : 0u)) & 15u) return GEMM_W4A4_EALIGN;
   if ((uintptr_t(a->lse) | uintptr_t(a->lens) | (keys ? uintptr_t(a->table) : 0u)) & 3u) return GEMM_W4A4_EALIGN;
   const PagedPlan pl = paged_plan(a);
-  if (pl.whole >= int64_t(1) << 24) return GEMM_W4A4_EINVAL;   // (a launch holds fewer than 2^32 threads)
+  // (a launch holds fewer than 2^32 threads; by the smaller tiles, so that what is refused does not go by the plan)
+  constexpr int kRows = FewAttn<128>::ROWS;
+  if ((int64_t(pl.rows_all) + kRows - 1) / kRows * a->batch * a->kv_heads >= int64_t(1) << 24) return GEMM_W4A4_EINVAL;
   if (pl.bytes > 0) {
     if (!a->workspace || a->workspace_bytes < pl.bytes) return GEMM_W4A4_ESCRATCH;
     if (uintptr_t(a->workspace) & 15u) return GEMM_W4A4_EALIGN;
@@ -155,11 +172,11 @@ static int paged_run(const paged_attention_t* a, void* stream) {
   p.per_seq = pl.tiles * a->kv_heads;
   p.even = pl.even;
   p.c = a->scale * 1.4426950408889634f;
-  int tile_rows = FewAttn<128>::ROWS;
+  int tile_rows = pl.rows;
   void* args[] = {&p, &tile_rows};
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t grid = pl.whole + int64_t(pl.cut) * pl.parts;
-  hipError_t e = hipLaunchKernel(a->f16 ? paged_of<true>(D) : paged_of<false>(D), dim3(unsigned(grid)), dim3(256), args, 0, st);
+  hipError_t e = hipLaunchKernel(a->f16 ? paged_of<true>(pl.few, D) : paged_of<false>(pl.few, D), dim3(unsigned(grid)), dim3(256), args, 0, st);
   if (e == hipSuccess && pl.cut > 0) {
     const int rows = std::min(tile_rows, pl.rows_all);
     e = hipLaunchKernel(a->f16 ? reinterpret_cast<const void*>(attention_join_kernel<true, Attend::kPaged>)

@@ -285,6 +285,7 @@ __device__ __forceinline__ Share share_of(const AttnParams& p, int& rows, int& o
   w.tile = id / p.pairs;
   w.b = w.pair / p.kv_heads;
   w.kvh = w.pair - w.b * p.kv_heads;
+  if constexpr (A == Attend::kPaged) w.tile = p.per_seq / p.kv_heads - 1 - w.tile;   // the last rows see the most keys
   const int len = __builtin_amdgcn_readfirstlane(keys_of(p, w.b));
   w.first = 0;
   w.len = len;
@@ -321,16 +322,21 @@ struct Pages {
     const int64_t at = int64_t(from) + (threadIdx.x & 63);
     entries = at * p.page_size < p.kv_len ? p.table[int64_t(b) * p.table_stride + at] : -1;
   }
+  __device__ __forceinline__ int place_of(int key) const { return int(__umulhi(uint32_t(key), p.page_magic) >> p.page_shift); }
   // the page that holds key `key` of the sequence: its number in the cache, -1 where there is none
   __device__ __forceinline__ int page_of(int key) {
-    const int i = int(__umulhi(uint32_t(key), p.page_magic) >> p.page_shift);
+    const int i = place_of(key);
     if (i < page0 || i >= page0 + 64) look(i);
-    const int e = __builtin_amdgcn_readlane(entries, i - page0);
+    return held(key);
+  }
+  // likewise of a key whose entry is held
+  __device__ __forceinline__ int held(int key) const {
+    const int e = __builtin_amdgcn_readlane(entries, place_of(key) - page0);
     return e >= 0 && e < p.pages ? e : -1;
   }
   // the bytes from a cache's start to that key, `stride` a token
   __device__ __forceinline__ int64_t key_at(int key, int page, int64_t page_stride, uint32_t stride) const {
-    const int i = int(__umulhi(uint32_t(key), p.page_magic) >> p.page_shift);
+    const int i = place_of(key);
     return int64_t(page) * page_stride * 2 + int64_t(key - i * p.page_size) * stride;
   }
 };
@@ -783,6 +789,9 @@ struct WideAttn {
 //
 // Packed sequences with the mask: a row sees the keys up to its own; a tile's steps end
 // with its last row's, and only the steps past its first row's are masked.
+//
+// Paged: likewise; a wave's load of 4 or 8 keys lies in 16 of one page. A sequence with an
+// entry outside the cache masks every step.
 template <bool F16, class C, Attend A>
 __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const AttnParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
@@ -795,9 +804,15 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
   // same units (4352 x 4608 keys, 24 heads of 128: 265 to 256 us).
   if (blockIdx.x & 256) __builtin_amdgcn_s_setprio(2);
   int rows = p.rows, origin = 0;   // rows of the sequence; packed: its first token
-  const Share w = share_of<C, A, C::KT>(p, rows, origin);
+  Share w = share_of<C, A, C::KT>(p, rows, origin);
   if (w.idle) return;
-  const int b = w.b, kvh = w.kvh, len = w.len, D = p.D;
+  const int b = w.b, kvh = w.kvh, D = p.D;
+  int before = 0;   // paged: keys of the share that the sequence's first new token sees (with those up to it)
+  if constexpr (A == Attend::kPaged) {
+    before = __builtin_amdgcn_readfirstlane(keys_of(p, b)) - p.q_len + 1 - w.first;   // (all keys and new tokens are fewer than 2^31)
+    w.len = max(0, min(w.len, before + (min(rows, (w.tile + 1) * C::ROWS) - 1) / p.group));
+  }
+  const int len = w.len;
   const int n = (len + C::KT - 1) / C::KT;
 
   const int row = w.tile * C::ROWS + wave * 32 + l32;
@@ -810,6 +825,20 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
       lim = tok - origin + 1;
       lim0 = w.tile * C::ROWS / p.group + 1;
     }
+  Pages pages{p, b};
+  bool holes = false;   // paged: an entry of the share's keys is no page
+  if constexpr (A == Attend::kPaged) {
+    lim = min(len, before + tok);
+    lim0 = max(0, min(len, before + w.tile * C::ROWS / p.group));
+    const int first = w.first / p.page_size;
+    for (int i = first; int64_t(i) * p.page_size < int64_t(w.first) + len; i += 64) {
+      pages.look(i);
+      holes |= __builtin_amdgcn_ballot_w64(int64_t(i + lane) * p.page_size < int64_t(w.first) + len &&
+                                           (pages.entries < 0 || pages.entries >= p.pages)) != 0;
+    }
+    if (pages.page0 != first) pages.look(first);
+    if (holes) lim0 = 0;
+  }
   u32x4 qv[DK];
   {
     const uint16_t* q = p.q + int64_t(b) * p.qs[0] + int64_t(tok) * p.qs[1] + int64_t(hq) * p.qs[2];
@@ -826,22 +855,64 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
   const int kc = k_chunk<C>(dr, dp), vc = v_chunk<C>(dr, dp);
   const uint32_t kst = uint32_t(p.ks[1]) * 2u, vst = uint32_t(p.vs[1]) * 2u;
   const bool klive = kc * 8 < D, vlive = vc * 8 < D;
-  const uint32_t koff = klive ? uint32_t(dr) * kst + uint32_t(kc) * 16u : 0xFFFFFFF0u, kstep = klive ? C::RPR * kst : 0u;
-  const uint32_t voff = vlive ? uint32_t(dr) * vst + uint32_t(vc) * 16u : 0xFFFFFFF0u, vstep = vlive ? C::RPR * vst : 0u;
-  const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k + int64_t(b) * p.ks[0] + int64_t(kvh) * p.ks[2] + int64_t(origin + w.first) * p.ks[1]);
-  const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v + int64_t(b) * p.vs[0] + int64_t(kvh) * p.vs[2] + int64_t(origin + w.first) * p.vs[1]);
+  const int in = A == Attend::kPaged ? dr & 15 : dr;   // row of what the load's range holds
+  const uint32_t koff = klive ? uint32_t(in) * kst + uint32_t(kc) * 16u : 0xFFFFFFF0u, kstep = klive ? C::RPR * kst : 0u;
+  const uint32_t voff = vlive ? uint32_t(in) * vst + uint32_t(vc) * 16u : 0xFFFFFFF0u, vstep = vlive ? C::RPR * vst : 0u;
+  const uint16_t *kh = p.k + int64_t(kvh) * p.ks[2], *vh = p.v + int64_t(kvh) * p.vs[2];
+  if constexpr (A != Attend::kPaged) {
+    kh += int64_t(b) * p.ks[0] + int64_t(origin + w.first) * p.ks[1];
+    vh += int64_t(b) * p.vs[0] + int64_t(origin + w.first) * p.vs[1];
+  }
+  const uint8_t *kb = reinterpret_cast<const uint8_t*>(kh), *vb = reinterpret_cast<const uint8_t*>(vh);
   const uint32_t lds0 = lds_address(smem) + wave * 1024;
   // Tile t of K (to ring place t % RING) or V; tiles past the last key are
   // empty ranges: zeros (by a mask and no branch, so that a step stays one block).
-  auto load = [&](const uint8_t* base, uint32_t stride, uint32_t off, uint32_t step, int t, uint32_t to) __attribute__((always_inline)) {
+  auto load = [&](const uint8_t* base, int64_t page_stride, uint32_t stride, uint32_t off, uint32_t step, int t, uint32_t to) __attribute__((always_inline)) {
+    if constexpr (A == Attend::kPaged) {
+#pragma unroll
+      for (int u = 0; u < C::ROUNDS; ++u) {
+        const int r0 = t * C::KT + (C::RPR == 16 ? 16 * u : 16 * (wave >> 1)), rows = min(len - r0, 16);
+        const int page = pages.held(w.first + r0);
+        const uint32_t any = uint32_t(~(page >> 31)) & uint32_t(-rows >> 31);
+        const u32x4 rs = range_desc(base + pages.key_at(w.first + r0, max(page, 0), page_stride, stride),
+                                    (uint32_t(rows - 1) * stride + uint32_t(D) * 2u) & any);
+        load_to_lds(rs, off, uint32_t(__builtin_amdgcn_readfirstlane(lds0 + to + u * C::RPR * C::ROWB)));
+      }
+      return;
+    }
     const int rows = min(len - t * C::KT, C::KT);
     const uint32_t any = uint32_t(-rows >> 31);   // all ones where rows > 0
     const u32x4 rs = range_desc(base + int64_t(t * C::KT) * stride, (uint32_t(rows - 1) * stride + uint32_t(D) * 2u) & any);
 #pragma unroll
     for (int u = 0; u < C::ROUNDS; ++u) load_to_lds(rs, off + u * step, lds0 + to + u * C::RPR * C::ROWB);
   };
-  auto load_k = [&](int t, int ring) __attribute__((always_inline)) { load(kb, kst, koff, kstep, t, ring * C::TILE); };
-  auto load_v = [&](int t, int ring) __attribute__((always_inline)) { load(vb, vst, voff, vstep, t, VOFF + ring * C::TILE); };
+  // Paged: the ranges that steps j .. j + 3 load, j a multiple of 4, made by a lane each: 16 keys
+  // of K by lanes 0 .. 7, of V by 8 .. 15 (by scalar instructions in each step 2048 tokens over 8000
+  // keys take 279 us, and with a branch for the table's next entries 360; so 221).
+  uint32_t range_low = 0, range_high = 0, range_bytes = 0;
+  auto ranges = [&](int j) __attribute__((always_inline)) {
+    if (pages.place_of(w.first + (j + 8) * C::KT) >= pages.page0 + 64) pages.look(pages.place_of(w.first + j * C::KT));
+    const bool val = lane & 8;
+    const int r0 = (j + (val ? 2 : 4)) * C::KT + 16 * (lane & 7), key = w.first + r0, i = pages.place_of(key), rows = min(len - r0, 16);
+    const int e = __builtin_amdgcn_ds_bpermute((i - pages.page0) * 4, pages.entries);
+    const bool any = rows > 0 && e >= 0 && e < p.pages;
+    const uint32_t stride = val ? vst : kst;
+    const uint64_t at = reinterpret_cast<uint64_t>(val ? vb : kb) + pages.key_at(key, any ? e : 0, val ? p.vs[0] : p.ks[0], stride);
+    range_low = uint32_t(at);
+    range_high = uint32_t(at >> 32) & 0xFFFFu;
+    range_bytes = any ? uint32_t(rows - 1) * stride + uint32_t(D) * 2u : 0u;
+  };
+  auto load_range = [&](int from, uint32_t off, uint32_t to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < C::ROUNDS; ++u) {
+      const int at = from + (C::RPR == 16 ? u : wave >> 1);
+      const u32x4 rs{uint32_t(__builtin_amdgcn_readlane(range_low, at)), uint32_t(__builtin_amdgcn_readlane(range_high, at)),
+                     uint32_t(__builtin_amdgcn_readlane(range_bytes, at)), 0x00020000u};
+      load_to_lds(rs, off, uint32_t(__builtin_amdgcn_readfirstlane(lds0 + to + u * C::RPR * C::ROWB)));
+    }
+  };
+  auto load_k = [&](int t, int ring) __attribute__((always_inline)) { load(kb, p.ks[0], kst, koff, kstep, t, ring * C::TILE); };
+  auto load_v = [&](int t, int ring) __attribute__((always_inline)) { load(vb, p.vs[0], vst, voff, vstep, t, VOFF + ring * C::TILE); };
 
   // this lane's LDS addresses in the rings' first tiles, by slot
   uint32_t kaddr[DK], vaddr[DT];
@@ -883,6 +954,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
 #pragma unroll
         for (int i = 4 * part; i < 4 * part + 4; ++i)
           if (key0 + 8 * (i >> 2) + 4 * h + (i & 3) >= lim) s[i] = -INFINITY;
+        if constexpr (A == Attend::kPaged)
+          if (holes && pages.held(w.first + key0 + 8 * (part & 2)) < 0)
+#pragma unroll
+            for (int i = 4 * part; i < 4 * part + 4; ++i) s[i] = -INFINITY;
       }
       float t = part == 0 ? s[0] : top;
 #pragma unroll
@@ -937,6 +1012,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
   // them; K tile j + 4 and V tile j + 2 are first read at that step's end.
   auto step = [&]<bool TAIL, int R>(int j) __attribute__((always_inline)) {
     constexpr int P = R & 1;
+    if constexpr (A == Attend::kPaged && R == 0) ranges(j);
     static_for<0, MFMAS>([&]<int I>() __attribute__((always_inline)) {
       constexpr int i = I / 2;
       __builtin_amdgcn_sched_barrier(0);
@@ -955,8 +1031,13 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
       static_for<first_part(I), first_part(I + 1)>([&]<int PART>() __attribute__((always_inline)) {
         soft.template operator()<TAIL>(PART, sc[P], pv[P], j * C::KT);
       });
-      if constexpr (I == MFMAS / 2) load_k(j + 4, R);
-      if constexpr (I == MFMAS / 2 + 1) load_v(j + 2, (R + 2) & 3);
+      if constexpr (A == Attend::kPaged) {
+        if constexpr (I == MFMAS / 2) load_range(2 * R, koff, R * C::TILE);
+        if constexpr (I == MFMAS / 2 + 1) load_range(8 + 2 * R, voff, VOFF + ((R + 2) & 3) * C::TILE);
+      } else {
+        if constexpr (I == MFMAS / 2) load_k(j + 4, R);
+        if constexpr (I == MFMAS / 2 + 1) load_v(j + 2, (R + 2) & 3);
+      }
     });
     __builtin_amdgcn_sched_barrier(0);
     // (the compiler would move the weights past the branch, away from the MFMAs)
@@ -1013,7 +1094,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
       if (j + 2 < n) step.template operator()<true, 2>(j + 2);
       if (j + 3 < n) step.template operator()<true, 3>(j + 3);
       j += 4;
-    } while (A == Attend::kPacked && j < n);
+    } while (A != Attend::kDense && j < n);
     wait_vm<0>();
     // products of the last 32 keys
     const int last = (n - 1) & 3;
@@ -1025,7 +1106,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
   }
 
   const AttnParams& pe = A == Attend::kDense ? p : params_again();
-  if constexpr (A == Attend::kPacked)
+  if constexpr (A != Attend::kDense)
     if (lim0 < len && any_not_finite(o)) see_again<F16, C, A, 1>(o, qv, pe, w, origin, m, lim, lim0, 0);
   if (row >= rows) return;
   l = other_sum(l);
@@ -1038,6 +1119,7 @@ template <bool F16, Attend A>
 __global__ __launch_bounds__(256) void attention_join_kernel(const AttnParams p, int tile_rows) {
   const int per = p.D / 4, nth = blockIdx.y, id = p.whole + nth;
   int pair = id % p.pairs, tile = id / p.pairs, parts = p.parts;
+  if constexpr (A == Attend::kPaged) tile = p.per_seq / p.kv_heads - 1 - tile;
   int64_t slot = int64_t(nth) * p.parts;
   if (p.even) {   // nth: (sequence, row tile, key head)
     const EvenParts e = even_parts(p, -1, nth / p.per_seq);

@@ -695,8 +695,8 @@ int packed_attention(const packed_attention_t* args, void* stream);
  * page_size a multiple of PAGED_ATTENTION_PAGE_MULTIPLE; table_width * page_size and q_len below
  * 2^30 - CROSS_ATTENTION_PAST_END; batch * kv_heads times the tiles of 32 rows of each below 2^24; scale, head_dim, heads, strides (q and out: batch, token, head; caches: page,
  * token, head; table: batch), alignment and limits of rows as for cross_attention, v_cache's token
- * stride at least head_dim. Made for few new tokens: every 32 rows (token, query head of
- * a key head) read the keys anew. batch, q_len or q_heads 0: nothing is enqueued; pages or
+ * stride at least head_dim. Every 32 rows (token, query head of a key head) read the
+ * keys anew, past 64 rows every 128. batch, q_len or q_heads 0: nothing is enqueued; pages or
  * table_width 0: no keys, caches and table may be NULL.
  *
  * workspace: paged_attention_workspace bytes, 16-byte aligned, that nothing else uses until the call's

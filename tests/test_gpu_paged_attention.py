@@ -220,3 +220,80 @@ def test_repeats_streams_and_graph():
         eager = [w4.paged_attention(hq * f, kc, vc, ht, hl) for f in (1, 2)]
         torch.cuda.synchronize()
         assert torch.equal(kept, eager[0]) and torch.equal(again, eager[1])
+
+
+@pytest.mark.parametrize("page", [16, 48, 128])
+@pytest.mark.parametrize("Q,HQ,HKV,D,dtype", [(40, 4, 4, 128, "bf16"), (129, 3, 3, 64, "f16"), (300, 6, 2, 96, "bf16"), (65, 16, 1, 40, "f16"),
+                                              (257, 2, 1, 128, "f16"), (33, 5, 5, 8, "bf16")])
+def test_long_pieces_of_prompts(Q, HQ, HKV, D, dtype, page):
+    """Many new tokens over a cache that holds more, just them, fewer or none."""
+    for lens in ([Q + 700, Q, Q - 20, 0], [Q + 1], [Q + 31, Q + 1500]):
+        print(f"case: {Q} {HQ}/{HKV} D{D} page {page} {lens} {dtype}", flush=True)
+        check(*inputs(len(lens), Q, HQ, HKV, D, page, lens, dtype), f"{Q} {lens}")
+
+
+def test_long_pieces_over_a_wide_table():
+    """A table past the length from which on parts are even, and more tiles than compute units."""
+    for B, lens in ((1, [6000]), (2, [5000, 100]), (40, [150 + 7 * b for b in range(40)])):
+        q, kc, vc, table, l = inputs(B, 140, 8, 4, 64, 16, lens, "bf16")
+        wide = torch.full((B, 600), 2**30, dtype=torch.int32, device=DEV)
+        wide[:, :table.shape[1]] = table
+        check(q, kc, vc, wide, l, f"{lens[:2]}")
+        check(q, kc, vc, table, l, f"{lens[:2]}")
+
+
+def test_long_pieces_with_entries_that_are_no_page():
+    for bad in (-1, 2**31 - 1, -2**31, 10**6):
+        for D in (64, 128):
+            q, kc, vc, table, lens = inputs(3, 50, 6, 2, D, 16, [1400, 90, 70], "bf16")
+            table[0, 3], table[0, 70], table[0, 87], table[1, 0] = bad, bad, bad, bad
+            table[2, :] = bad
+            got, lse = check(q, kc, vc, table, lens, f"{bad}")
+            assert (got[2] == 0).all() and (lse[2] == float("-inf")).all()
+        check(q, kc, vc, table, torch.tensor([2**31 - 1, -5, 2**30], dtype=torch.int32, device=DEV), "lengths past the table")
+
+
+@pytest.mark.parametrize("Q,HQ,HKV", [(20, 6, 2), (150, 6, 2)])
+def test_what_a_row_of_many_does_not_see(Q, HQ, HKV):
+    """Infinities and NaN in a new token's key or value change no earlier one, with every entry a page and with one that is none."""
+    for dtype in ("bf16", "f16"):
+        for hole in (False, True):
+            q, kc, vc, table, lens = inputs(2, Q, HQ, HKV, 72, 16, [Q + 200, Q + 5], dtype)
+            if hole:
+                table[:, 2] = -1
+            y, _, bound, _ = ref.paged_attention_ref(*(values_of(t) for t in (q, kc, vc)), table.cpu().numpy(), lens.cpu().numpy(), dtype=dtype)
+            want = w4.paged_attention(q, kc, vc, table, lens)
+            for value in (float("nan"), float("inf")):
+                for cache, i in ((vc, Q - 1), (vc, 7), (kc, 11)):
+                    c, key = cache.clone(), 200 + i
+                    c[table[0, key // 16].long(), key % 16, :, 5] = value
+                    got = w4.paged_attention(q, c if cache is kc else kc, c if cache is vc else vc, table, lens)
+                    assert_within(values_of(got)[0, :i], y[0, :i], bound[0, :i], f"{value} in new token {i}")
+                    assert torch.equal(got[1], want[1])
+                    if cache is vc:
+                        assert not torch.isfinite(got[0, i:, :, 5]).any() and torch.isfinite(got[0, i:, :, 6:]).all()
+
+
+def test_a_piece_is_the_packed_prompt():
+    """A prompt as new tokens of an empty cache, whole and in pieces, within the roundings of the packed one; replayed."""
+    T, HQ, HKV, D, page = 900, 8, 2, 128, 64
+    q, kc, vc, table, lens = inputs(1, T, HQ, HKV, D, page, [T], "bf16")
+    whole, _ = check(q, kc, vc, table, lens, "whole")
+    y, _, bound, _ = ref.paged_attention_ref(*(values_of(t) for t in (q, kc, vc)), table.cpu().numpy(), lens.cpu().numpy(), dtype="bf16")
+    for at, to in ((0, 300), (300, 337), (337, 900)):
+        piece = w4.paged_attention(q[:, at:to], kc, vc, table, torch.tensor([to], dtype=torch.int32, device=DEV))
+        assert_within(values_of(piece), y[:, at:to], bound[:, at:to], f"{at} to {to}")
+    flat = torch.cat([c[table[0, :15].long()].reshape(-1, HKV, D)[:T][None] for c in (kc, vc)])
+    packed = w4.packed_attention(q[0], flat[0].contiguous(), flat[1].contiguous(), torch.tensor([0, T], dtype=torch.int32, device=DEV))
+    assert_within(values_of(packed), y[0], bound[0], "packed")
+    hq, hl = q.clone(), lens.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept = w4.paged_attention(hq, kc, vc, table, hl)
+    for i in range(3):
+        hq.copy_(q * (1 + i))
+        hl.fill_(T - 200 * i)
+        g.replay()
+        eager = w4.paged_attention(hq, kc, vc, table, hl)
+        torch.cuda.synchronize()
+        assert torch.equal(kept, eager)
