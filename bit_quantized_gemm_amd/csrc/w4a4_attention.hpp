@@ -906,8 +906,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
 #pragma unroll
     for (int u = 0; u < C::ROUNDS; ++u) {
       const int at = from + (C::RPR == 16 ? u : wave >> 1);
-      const u32x4 rs{uint32_t(__builtin_amdgcn_readlane(range_low, at)), uint32_t(__builtin_amdgcn_readlane(range_high, at)),
-                     uint32_t(__builtin_amdgcn_readlane(range_bytes, at)), 0x00020000u};
+      u32x4 rs{uint32_t(__builtin_amdgcn_readlane(range_low, at)), uint32_t(__builtin_amdgcn_readlane(range_high, at)),
+               uint32_t(__builtin_amdgcn_readlane(range_bytes, at)), 0x00020000u};
+      settle_desc(rs);
       load_to_lds(rs, off, uint32_t(__builtin_amdgcn_readfirstlane(lds0 + to + u * C::RPR * C::ROWB)));
     }
   };
