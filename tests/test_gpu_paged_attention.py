@@ -297,3 +297,50 @@ def test_a_piece_is_the_packed_prompt():
         eager = w4.paged_attention(hq, kc, vc, table, hl)
         torch.cuda.synchronize()
         assert torch.equal(kept, eager)
+
+
+def test_long_pieces_past_32_bits_and_strided():
+    """Pages on both sides of every 2^32-byte border of a cache, keys and values side by side, heads before places."""
+    H, D, page, Q = 4, 72, 32, 90
+    n = 5 * page - 3
+    k, v = (torch.randn(n, H, D, device=DEV).half() for _ in range(2))
+    at, lens = torch.arange(n, device=DEV), torch.tensor([n], dtype=torch.int32, device=DEV)
+    kc, vc = (torch.full((5, page, H, D), float("nan"), dtype=torch.float16, device=DEV) for _ in range(2))
+    w4.cache_append(k, v, kc, vc, at)
+    q = torch.randn(1, Q, H, D, device=DEV).half()
+    order = torch.arange(5, dtype=torch.int32, device=DEV)[None]
+    want, _ = check(q, kc, vc, order, lens, "small")
+
+    pages = 2**33 // (4 * H * D * page) + 3
+    joint = torch.full((pages, 2, H, page, D), float("nan"), dtype=torch.float16, device=DEV)
+    far_k, far_v = joint[:, 0].transpose(1, 2), joint[:, 1].transpose(1, 2)
+    border = 2**32 // (4 * H * D * page)
+    table = torch.tensor([[pages - 1, border - 1, 0, border, 2 * border, 7]], dtype=torch.int32, device=DEV)
+    w4.cache_append(k, v, far_k, far_v, table[0, at // page].long() * page + at % page)
+    wide = torch.zeros(1, Q, H + 2, D + 8, dtype=torch.float16, device=DEV)
+    wide[:, :, 1:1 + H, 8:] = q
+    out = torch.full((1, Q, H + 1, D), 5.0, dtype=torch.float16, device=DEV)
+    w4.paged_attention(wide[:, :, 1:1 + H, 8:], far_k, far_v, table, lens, out=out[:, :, :H])
+    assert torch.equal(out[:, :, :H], want) and (out[:, :, H] == 5.0).all()
+
+
+def test_workspace_of_long_pieces_between_guards():
+    for B, Q, n in ((1, 70, 5000), (3, 140, 900), (33, 40, 700)):
+        q, kc, vc, table, lens = inputs(B, Q, 8, 4, 64, 16, [max(0, n - 37 * b) for b in range(B)], "bf16")
+        want = w4.paged_attention(q, kc, vc, table, lens, return_lse=True)
+        for fill in (0x00, 0xFF):
+            out, lse = torch.empty_like(q), torch.empty_like(want[1])
+            a = w4.PagedAttentionArgs()
+            a.q, a.k_cache, a.v_cache, a.out, a.lse, a.table, a.lens = (t.data_ptr() for t in (q, kc, vc, out, lse, table, lens))
+            a.batch, a.q_len, a.q_heads, a.kv_heads, a.head_dim = B, Q, 8, 4, 64
+            a.pages, a.page_size, a.table_width, a.table_stride, a.scale = kc.shape[0], 16, table.shape[1], table.shape[1], 0.125
+            for f, t in (("q_stride", q), ("k_stride", kc), ("v_stride", vc), ("out_stride", out)):
+                for i in range(3):
+                    getattr(a, f)[i] = t.stride(i)
+            need = w4.paged_attention_workspace(a)
+            buf = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device=DEV)
+            buf[4096:4096 + need] = fill
+            a.workspace, a.workspace_bytes = buf.data_ptr() + 4096, need
+            assert need > 0 and w4.paged_attention_raw(a, torch.cuda.current_stream().cuda_stream) == w4.OK
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+            assert (buf[:4096] == 0xA5).all() and (buf[4096 + need:] == 0xA5).all()
