@@ -64,7 +64,11 @@ static PagedPlan paged_plan(const paged_attention_t* a) {
   pl.whole = int64_t(pl.tiles) * a->batch * a->kv_heads;
   pl.parts = 1;
   const int left = int(pl.whole % kNumCUs);
-  if (left > 0) {
+  // A prompt's own keys: the tiles differ in length by the mask, the short ones fill the last round, and parts
+  // of them only cost the join (us, cut and not: 2048 tokens over as many 60 and 52, 1600 47 and 40, 2048 of
+  // 24 key heads over 4096 113 and 110; but 2048 over 8000 207 and 215, 1408 169 and 195, 1700 over 6000 142 and 153).
+  const bool own_keys = !pl.few && pl.whole >= kNumCUs && int64_t(a->table_width) * a->page_size < int64_t(a->q_len) * 3;
+  if (left > 0 && !own_keys) {
     const int slots = pl.whole < kNumCUs ? 2 * kNumCUs : kNumCUs;
     const int parts = std::min(slots / left, a->table_width * a->page_size / kMinPart);
     if (parts > 1) {

@@ -344,3 +344,12 @@ def test_workspace_of_long_pieces_between_guards():
             assert need > 0 and w4.paged_attention_raw(a, torch.cuda.current_stream().cuda_stream) == w4.OK
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
             assert (buf[:4096] == 0xA5).all() and (buf[4096 + need:] == 0xA5).all()
+
+
+def test_prompts_of_more_tiles_than_compute_units():
+    """Whole tiles where the table holds little more than the prompt, parts of the last ones where it is wide."""
+    q, kc, vc, table, lens = inputs(1, 1030, 34, 34, 64, 16, [1030], "bf16")
+    wide = torch.full((1, 300), -1, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    check(q, kc, vc, table, lens, "its own keys")
+    check(q, kc, vc, wide, lens, "a wide table")
