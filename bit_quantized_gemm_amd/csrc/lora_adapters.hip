@@ -198,11 +198,14 @@ __device__ __forceinline__ void split8(const float (&v)[8], u32x4& high, u32x4& 
   }
 }
 
-// binary16: the power of two by which a row whose largest value is `top` is multiplied
-// before the split, which takes that to 2^14 .. 2^15, and its inverse.
+// binary16: the power of two by which a row whose largest finite value is `top` is multiplied
+// before the split, which takes that to 2^14 .. 2^15, and its inverse. (An infinity stays
+// one under any factor, and may not leave the row's other values past the type's range:
+// opposite infinities would be a NaN.)
+__device__ __forceinline__ float finite_size(float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.f; }
 __device__ __forceinline__ void row_factor(float top, float& to, float& back) {
   to = back = 1.f;
-  if (top > 0.f && top < INFINITY) {
+  if (top > 0.f) {
     const int e = max(__builtin_amdgcn_frexp_expf(top), -100) - 15;
     to = __builtin_amdgcn_ldexpf(1.f, -e);
     back = __builtin_amdgcn_ldexpf(1.f, e);
@@ -366,7 +369,7 @@ __global__ __launch_bounds__(512) void adapters_join_kernel(const AdaptParams p)
     const int steps = rank_steps(rank_of(p, p.adapter[row]));
     float m = 0.f, to, back;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_size(v[e]));
     if (tid < 32) top[tid] = 0;
     __syncthreads();
     if (t < steps) atomicMax(&top[r], __builtin_bit_cast(uint32_t, m));   // (of magnitudes, in any order the same)
@@ -504,7 +507,7 @@ __global__ __launch_bounds__(256, KT > 4 ? (SLICED ? 1 : 2) : SLICED ? 2 : KT > 
 #pragma unroll
             for (int k = 0; k < NT; ++k)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(low[k][e]));
+              for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(low[k][e]));
             row_factor(other_max(top), to, back);
 #pragma unroll
             for (int k = 0; k < NT; ++k)
