@@ -359,17 +359,20 @@ __device__ __forceinline__ float rounded_product(float a, float b) {
   return a * b;
 }
 
-// The sums o of a lane's row again, key by key, leaving out the keys that the row does
-// not see. In the matrix product those have weight 0, which is not enough where a value
-// is an infinity or a NaN: 0 times it is NaN. Taken when a sum is one and a value that some row
-// does not see is one; slow (some 300 instructions a key).
-// `key` calls its argument with every key's index and the addresses of its k and v rows.
+// A lane's row again, key by key, leaving out the keys that it does not see: its sums o, maximum m
+// and (in the lower half of the wave) sum of weights l. In the matrix product those keys have weight 0, which
+// is not enough where a value is an infinity or a NaN: 0 times it is NaN. Taken when a sum is one
+// and a value that some row does not see is one; slow (some 300 instructions a key).
+// m and l come from the scores used here: theirs are summed in another order than the matrix
+// instruction's, and of large ones a weight would differ by any factor from the one in l.
+// `keys` calls its argument with every key's index and the addresses of its k and v rows.
 template <bool F16, class C, class F>
-__device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x4 (&qv)[C::DP / 16], int D, float c, float m,
+__device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x4 (&qv)[C::DP / 16], int D, float c, float& m, float& l,
                                                        int lim, F&& keys) {
   constexpr int DK = C::DP / 16, DT = C::DP / 32;
   const int h = (threadIdx.x & 63) >> 5;
-  const float ms = m == -INFINITY ? 0.f : m;
+  m = -INFINITY;
+  l = 0.f;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -390,9 +393,21 @@ __device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x
       __builtin_amdgcn_sched_barrier(0);   // (one load at a time: registers)
     }
     s = other_sum(s);
-    const float x = fabsf(ms) > kFar ? rounded_product(s, c) - ms : __builtin_fmaf(s, c, -ms);
-    const float w = widen<F16>(narrow<F16>(__builtin_amdgcn_exp2f(x)));
-    if (j < lim)
+    const float far = rounded_product(s, c), mn = j < lim ? fmaxf(m, far) : m;
+    const float ms = mn == -INFINITY ? 0.f : mn;
+    if (__builtin_amdgcn_ballot_w64(mn != m)) {
+      const float alpha = __builtin_amdgcn_exp2f(m - ms);
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+    }
+    m = mn;
+    const float e0 = __builtin_amdgcn_exp2f(fabsf(ms) > kFar ? far - ms : __builtin_fmaf(s, c, -ms));
+    const float w = widen<F16>(narrow<F16>(e0));
+    if (j < lim) {
+      l += h == 0 ? e0 : 0.f;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -405,6 +420,7 @@ __device__ __forceinline__ void careful_sums(f32x16 (&o)[C::DP / 32], const u32x
           o[d][i + 3] += w * widen<F16>(uint16_t(a.y >> 16));
           __builtin_amdgcn_sched_barrier(0);
         }
+    }
   });
 }
 
@@ -434,11 +450,11 @@ __device__ __forceinline__ bool any_not_finite(const f32x16 (&o)[DT]) {
   return __builtin_amdgcn_ballot_w64(!(z == 0.f)) != 0;
 }
 
-// The sums of a wave that are no numbers again, if a value that some row does not see is
+// A wave's rows again whose sums are no numbers, if a value that some row does not see is
 // none. The wave's keys: every WAVES-th tile of the share from `wave` on.
 template <bool F16, class C, Attend A, int WAVES>
 __device__ __forceinline__ void see_again(f32x16 (&o)[C::DP / 32], const u32x4 (&qv)[C::DP / 16], const AttnParams& p, const Share& w,
-                                          int origin, float m, int lim, int lim0, int wave) {
+                                          int origin, float& m, float& l, int lim, int lim0, int wave) {
   int len = __builtin_amdgcn_readfirstlane(w.len);
   asm volatile("" : "+s"(len));
   Pages pages{p, w.b};
@@ -454,7 +470,7 @@ __device__ __forceinline__ void see_again(f32x16 (&o)[C::DP / 32], const u32x4 (
     }
   };
   if (!keys_not_finite<F16>(max(lim0, 0), len, p.D, [&](int j) __attribute__((always_inline)) { return row(v, p.vs, j); })) return;
-  careful_sums<F16, C>(o, qv, p.D, p.c, m, lim, [&](auto&& key) __attribute__((always_inline)) {
+  careful_sums<F16, C>(o, qv, p.D, p.c, m, l, lim, [&](auto&& key) __attribute__((always_inline)) {
     for (int t = wave; t * C::KT < len; t += WAVES)
 #pragma unroll 1
       for (int j = t * C::KT; j < min(len, (t + 1) * C::KT); ++j) {
@@ -694,7 +710,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
   wait_vm<0>();
   const AttnParams& pe = A == Attend::kDense ? p : params_again();
   if constexpr (A != Attend::kDense)
-    if (lim0 < len && any_not_finite(o)) see_again<F16, C, A, C::WAVES>(o, qv, pe, w, origin, m, lim, lim0, wave);
+    if (lim0 < len && any_not_finite(o)) see_again<F16, C, A, C::WAVES>(o, qv, pe, w, origin, m, l, lim, lim0, wave);
   l = other_sum(l);
 
   // join the waves' keys: the others write their sums, maximum and sum; wave 0
@@ -1108,7 +1124,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_wide_kernel(const Att
 
   const AttnParams& pe = A == Attend::kDense ? p : params_again();
   if constexpr (A != Attend::kDense)
-    if (lim0 < len && any_not_finite(o)) see_again<F16, C, A, 1>(o, qv, pe, w, origin, m, lim, lim0, 0);
+    if (lim0 < len && any_not_finite(o)) see_again<F16, C, A, 1>(o, qv, pe, w, origin, m, l, lim, lim0, 0);
   if (row >= rows) return;
   l = other_sum(l);
   store_row<F16, C>(pe, o, m, l, w, wave * 32 + l32, tok, hq, h);
