@@ -156,12 +156,7 @@ static int paged_run(const paged_attention_t* a, void* stream) {
   p.table_stride = a->batch > 1 ? a->table_stride : 0;
   p.pages = a->pages;
   p.page_size = a->page_size;
-  // key / page_size for keys below 2^31: with 2^(n-1) < page_size <= 2^n the multiplier
-  // ceil(2^(31+n) / page_size) has 32 bits, and is too large by less than 2^n / page_size
-  int n = 4;
-  while ((int64_t(1) << n) < a->page_size) ++n;
-  p.page_magic = uint32_t(((uint64_t(1) << (31 + n)) + a->page_size - 1) / a->page_size);
-  p.page_shift = n - 1;
+  p.page_index = page_index(a->page_size);
   p.q_len = a->q_len;
   p.kv_len = keys ? a->table_width * a->page_size : 0;
   p.kv_heads = a->kv_heads;

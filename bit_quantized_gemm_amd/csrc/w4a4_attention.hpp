@@ -17,6 +17,7 @@
 #include "w4a4_common.hpp"
 #include "w4a4_half.hpp"
 #include "w4a4_host.hpp"
+#include "w4a4_page_index.hpp"
 #include "w4a4_strided.hpp"
 #include "w4a4_transpose.hpp"
 #include "w4a4_wave.hpp"
@@ -53,8 +54,7 @@ struct AttnParams {
   const int32_t* table;
   int64_t table_stride;
   int page_size, pages;
-  uint32_t page_magic;   // key / page_size = high 32 bits of key * page_magic, >> page_shift
-  int page_shift;
+  PageIndex page_index;
 };
 
 // The parameters, read once more: what only the end of a kernel needs and would be kept over
@@ -322,7 +322,7 @@ struct Pages {
     const int64_t at = int64_t(from) + (threadIdx.x & 63);
     entries = at * p.page_size < p.kv_len ? p.table[int64_t(b) * p.table_stride + at] : -1;
   }
-  __device__ __forceinline__ int place_of(int key) const { return int(__umulhi(uint32_t(key), p.page_magic) >> p.page_shift); }
+  __device__ __forceinline__ int place_of(int key) const { return p.page_index.of(key); }
   // the page that holds key `key` of the sequence: its number in the cache, -1 where there is none
   __device__ __forceinline__ int page_of(int key) {
     const int i = place_of(key);
