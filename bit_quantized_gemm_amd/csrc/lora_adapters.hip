@@ -639,7 +639,7 @@ static AdaptPlan adapt_plan(const lora_adapters_t* a) {
     pl.out_tiles = (a->rows + 63) / 64;
     const int64_t groups = (int64_t(a->N) + 255) / 256 * std::max(1, pl.out_tiles);
     // (one more than the adapters: the rows without one)
-    pl.out_slots = int(std::max<int64_t>(1, std::min<int64_t>(4 * kNumCUs / groups, std::min(std::min(a->adapters + 1, a->rows), 64))));
+    pl.out_slots = int(std::max<int64_t>(1, std::min({4 * kNumCUs / groups, int64_t(a->adapters) + 1, int64_t(a->rows), int64_t(64)})));
   }
   pl.bytes = pl.low_bytes = int64_t(pl.slices) * a->rows * pl.Rp * 4;
   if (pl.many) {
