@@ -339,7 +339,8 @@ def packed_attention(q, k, v, starts, causal=True, scale=None, return_lse=False,
     head); any strides that are multiples of 8 with a dense last dimension; head_dim a
     multiple of 8 up to ATTENTION_MAX_HEAD_DIM. starts int32 [sequences + 1] on the device: sequence
     s is the tokens starts[s] .. starts[s + 1] - 1 (may be none). A token sees its
-    sequence's tokens, when causal those up to itself. scale: default head_dim ** -0.5. Returns out [tokens,
+    sequence's tokens, when causal those up to itself. scale: default head_dim ** -0.5. Float32 throughout, but for the
+    weights exp(...), which are rounded to q's type for the product with v. Returns out [tokens,
     q_heads, head_dim] (allocated dense when None), and with return_lse also the
     float32 log-sum-exp [q_heads, tokens]; tokens in no sequence (padding behind the last) keep what an out that was
     given holds, and have no defined value in a result that was allocated. No gradient is recorded.
@@ -356,7 +357,8 @@ def paged_attention(q, k_cache, v_cache, table, lens, scale=None, return_lse=Fal
     PAGED_ATTENTION_PAGE_MULTIPLE; strides and heads as for cross_attention. table int32
     [batch, width] on the device: page table[b, i] holds the keys i * page_size .. of sequence b (no page in
     the cache: its keys are left out); lens int32 [batch] on the device: keys of each sequence, the new ones among them. New token
-    i sees the keys up to lens[b] - q_len + i; rows that see none give 0. scale: default head_dim ** -0.5. Returns out
+    i sees the keys up to lens[b] - q_len + i; rows that see none give 0. scale: default head_dim ** -0.5. Float32 throughout, but for the
+    weights exp(...), which are rounded to q's type for the product with v. Returns out
     [batch, q_len, q_heads, head_dim] (allocated dense when None), and with return_lse also the float32
     log-sum-exp [batch, q_heads, q_len] (-inf for rows that see no key). No gradient is recorded.
     """

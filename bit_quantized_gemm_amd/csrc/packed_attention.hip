@@ -67,9 +67,10 @@ static int packed_run(const packed_attention_t* a, void* stream) {
   // Few tiles leave compute units idle and wait out their keys one step after the other: there
   // 32-row tiles, whose waves share the keys. By the 128-row tiles to expect, a sequence's last
   // one counted half (both measured, us, 128-row tiles against 32-row ones; 24 heads on 8 of 128
-  // where no others are named). Fewer than 180: one prompt of 512 15.7 and 13.1, of 2048 with 8 heads of 64 32.9 and
-  // 17.3, 4096 with 4 heads 73.4 and 43.4, 532 + 250 + 117 + 102 with 16 of 72 14.6 and 12.8. More:
-  // one of 1024 25.2 and 27.4, eight of 256 16.1 and 30.4, 32 of 64 11.8 and 27.4.
+  // where no others are named). Fewer than 180: one prompt of 512 14.8 and 11.7, of 2048 with 8 heads of 64 32.1 and
+  // 17.5, 4096 with 4 heads 69.1 and 40.9, 532 + 250 + 117 + 102 with 16 of 72 13.0 and 12.3. More:
+  // one of 1024 22.8 and 24.4, eight of 256 15.1 and 26.5, 32 of 64 10.9 and 23.2. (One long prompt of few
+  // heads gains from 32-row tiles past it too: 8192 with 8 heads of 64 130 and 110.)
   constexpr int kWide = WideAttn<128>::ROWS, kFew = FewAttn<128>::ROWS, kFewTiles = 180;
   static_assert(WideAttn<64>::ROWS == kWide && WideAttn<96>::ROWS == kWide && FewAttn<64>::ROWS == kFew && FewAttn<96>::ROWS == kFew, "one tile height");
   const bool few = int64_t(a->tokens) * a->q_heads + int64_t(std::min(a->seqs, a->tokens)) * a->kv_heads * (kWide / 2) < int64_t(kFewTiles) * kWide;

@@ -3,7 +3,7 @@
 // whose loads of 16 keys find their page in the table, and their join.
 //
 // Few new tokens are bound by reading the cache, pieces of prompts by the matrix cores (2048 tokens
-// of 24 heads over 8000 keys: 221 us, 780 TFLOP/s of the unmasked scores). The keys of tiles that fill no round of the compute units
+// of 24 heads over 8000 keys: 204 to 221 us from card to card, 794 to 861 TFLOP/s of the unmasked scores). The keys of tiles that fill no round of the compute units
 // are cut into parts, since sequences' lengths are known only to the device; a
 // second launch joins them in order.
 #include <hip/hip_runtime.h>
@@ -42,18 +42,18 @@ static bool paged_sizes_ok(const paged_attention_t* a) {
 }
 
 // Which tiles are cut, as for cross_attention, into parts of at least a step of all waves
-// (kMinPart keys; three tokens over 1001 keys: 256 12.8 us, 128 11.3, 64 10.9; eight
-// sequences of 1000 15.4, 13.9 and 13.0, of 200 10.5, 11.5 and 11.8). Up to kShort
+// (kMinPart keys; three tokens over 1001 keys: 256 12.9 us, 128 11.3, 64 10.8; eight
+// sequences of 1000 16.4, 15.3 and 13.5, of 200 10.3, 11.0 and 11.6). Up to kShort
 // keys each sequence's own are cut into as many parts; past that parts have even length over the
 // sequences, which takes the device 2 us to work out (one token, us, even parts against own: eight sequences of
-// 1000 19.9 and 15.4, four of 3000 to 100 15.4 and 14.6; one of 300 in a table of 8192 14.1, own parts would leave
-// most of 64 empty).
+// 1000 to 650 15.6 and 14.1, four of 3000 to 100 14.9 and 14.3; one of 300 in a table of 8192, where most of its own
+// 64 parts are empty, 13.9 and 16.1).
 static PagedPlan paged_plan(const paged_attention_t* a) {
   constexpr int kShort = 4096;
   // 32-row tiles read the keys again for every 32 rows, but split them over their waves (us, 32-row
   // tiles against 128-row ones, 24 heads on 8 where no others are named): 64 rows of 2 sequences of 4000, 8 heads
-  // of 64 14.4 and 15.8, 48 rows of 32 of 1000 31.4 and 30.6; 66 rows of 8 of 1000 22.4 and 19.8, 120 of
-  // 32 59 and 32, 1536 over 4096 keys 74 and 50, over 512 19.7 and 22.2, 6144 over 8000 472 and 221.
+  // of 64 14.9 and 15.9, 48 rows of 32 of 1000 30.3 and 28.2; 66 rows of 8 of 1000 22.4 and 20.0, 120 of
+  // 32 58 and 30, 1536 over 4096 keys 69 and 45, over 512 19.0 and 21.8, 6144 over 8000 476 and 204.
   constexpr int kFewRows = 64;
   PagedPlan pl{};
   pl.rows_all = a->q_len * (a->q_heads / a->kv_heads);
@@ -65,8 +65,9 @@ static PagedPlan paged_plan(const paged_attention_t* a) {
   pl.parts = 1;
   const int left = int(pl.whole % kNumCUs);
   // A prompt's own keys: the tiles differ in length by the mask, the short ones fill the last round, and parts
-  // of them only cost the join (us, cut and not: 2048 tokens over as many 60 and 52, 1600 47 and 40, 2048 of
-  // 24 key heads over 4096 113 and 110; but 2048 over 8000 207 and 215, 1408 169 and 195, 1700 over 6000 142 and 153).
+  // of them only cost the join (us, cut and not: 2048 tokens over as many 59 and 51, 1600 47 and 40, 2048 of
+  // 24 key heads over 4096 110 and 107; but 2048 over 8000 204 and 210, 1408 162 and 192, 1700 over 6000 139 and 150).
+  // By the table's width, since lengths are on the device: in a table of three times its keys a prompt is cut.
   const bool own_keys = !pl.few && pl.whole >= kNumCUs && int64_t(a->table_width) * a->page_size < int64_t(a->q_len) * 3;
   if (left > 0 && !own_keys) {
     const int slots = pl.whole < kNumCUs ? 2 * kNumCUs : kNumCUs;

@@ -776,9 +776,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_few_kernel(const Attn
 //
 // Rings of four 32-key tiles of K and of V, loaded two steps before they are
 // read, one meeting of the workgroup a step. 4352 x 4608 keys, 24 heads of 128:
-// 246 to 282 us from card to card, 873 to 1003 TFLOP/s of the 1228 that a large
+// 246 to 282 us from card to card, 873 to 1003 TFLOP/s of the 1228 to 1386 that a large
 // product reaches; the matrix cores, the exponentials and the LDS reads share the
-// issue slots. 4096 x 512 keys: 34 to 39 us, 661 to 750 TFLOP/s, with 768 tiles for
+// issue slots. 4096 x 512 keys: 34 to 40 us, 644 to 750 TFLOP/s, with 768 tiles for
 // 512 places.
 //
 // The sums are rescaled only when a row's maximum has grown by more than
